@@ -56,7 +56,9 @@ typedef enum {
                                 That build waits for the device at the end of every call. */
 } moe_status_t;
 
-typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP8_E4M3 = 1, MOE_DT_FP4_E2M1 = 2 } moe_dtype_t;
+/* F32 and I8 are types of the operators around the experts (moe_block_norm, moe_router,
+ * moe_gemm_i8); moe_quant_act and moe_fused take the first three only. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP8_E4M3 = 1, MOE_DT_FP4_E2M1 = 2, MOE_DT_F32 = 3, MOE_DT_I8 = 4 } moe_dtype_t;
 
 /* Activation of the stage1 epilogue.  SITUV2 and SILU take act(g) * up as described above
  * (SILU: y = silu(g) * u, PR 4471 "Motivation").  NONE_TEST is a test hook: moe_fused runs
@@ -347,6 +349,192 @@ moe_status_t moe_fused_noalloc(const void *x, const uint8_t *x_scale, int32_t a_
                                int32_t tokens, int32_t topk, int32_t num_local_experts,
                                int32_t model_dim, int32_t inter_dim, const moe_act_params_t *act,
                                uint16_t *out_bf16, int32_t stages, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The rest of the layer: the norms before and after a block, the router with its balance loss,
+ * and the 8-bit integer product of a shared expert.  The conventions above hold for these too.
+ * Optional pointers are NULL when not given.  Outputs must not overlap inputs or each other
+ * except where a call allows it.  All sums, statistics and partial sums are fp32 (int32 for the
+ * integer product), no call uses atomics whose order changes a result, and equal calls on equal
+ * devices give equal bits.
+ * ------------------------------------------------------------------------------------------- */
+
+/* What a block's gate is shared by.  CHANNEL: fp32 [dim]; TOKEN: fp32 [tokens]; ELEMENT: bf16
+ * [tokens, dim]. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_ELEMENT = 3 } moe_gate_t;
+/* How it is applied: g itself or sigmoid(g). */
+typedef enum { MOE_GATE_RAW = 0, MOE_GATE_SIGMOID = 1 } moe_gate_act_t;
+
+/* Widest row of moe_block_norm. */
+#define MOE_NORM_MAX_DIM 16384
+/* Most partial sums of moe_block_norm_backward. */
+#define MOE_NORM_PARTS 512
+
+typedef struct {
+  const void *x;        /* [tokens, dim] residual stream, bf16 or fp32 (x_dt) */
+  const uint16_t *y;    /* [tokens, dim] bf16 output of a block, or NULL */
+  const float *w_post;  /* [dim] weight of the norm after the block, or NULL (no such norm) */
+  const void *gate;     /* by gate_kind; NULL iff MOE_GATE_NONE */
+  const float *w_pre;   /* [dim] weight of the norm before the next block, or NULL (no such norm) */
+  void *h;              /* out [tokens, dim] as x: the new residual stream, or NULL; may be x */
+  uint16_t *n;          /* out [tokens, dim] bf16 normed rows, or NULL */
+  void *q;              /* out: their codes (q_dt), or NULL */
+  void *q_scale;        /* out: their scales; NULL iff q is */
+  float *rstd;          /* out [2, tokens]: 1/rms(y) and 1/rms(h), for the backward pass, or NULL */
+  int32_t tokens, dim;
+  int32_t x_dt;         /* MOE_DT_BF16 or MOE_DT_F32 */
+  int32_t gate_kind;    /* moe_gate_t */
+  int32_t gate_act;     /* moe_gate_act_t */
+  int32_t q_dt;         /* MOE_DT_FP8_E4M3, MOE_DT_FP4_E2M1 or MOE_DT_I8; read only when q is given */
+  float scale;          /* of the block's output, finite */
+  float eps;            /* of both norms, finite and > 0 */
+} moe_block_norm_t;
+
+/* moe_block_norm -- the norm after one block, its gate, the residual sum and the norm before the
+ * next block, with the normed rows coded for what reads them, in one launch and one pass over
+ * the rows.  With rms(v) = sqrt(mean(v^2) + eps):
+ *     z = y / rms(y) * w_post  (z = y without w_post);   g = gate or sigmoid(gate), 1 without one
+ *     h = x + scale * g * z    (h = x without y);        n = h / rms(h) * w_pre
+ * computed in fp32 from the given rows; h, n and q are each rounded once, from fp32 (n and q come
+ * from h before its rounding).
+ *   q         FP8_E4M3, FP4_E2M1: codes and e8m0 scales of 1x32 blocks, as moe_quant_act writes them
+ *             (its rule applied to the fp32 values); dim % 32 == 0.  I8: codes [tokens, dim] and
+ *             fp32 scales [tokens], as moe_quant_i8; dim % 16 == 0.  With q every given tensor of
+ *             rows or channels is 16-byte aligned (else MOE_ERR_INVALID_ARG).
+ * Shapes: 1 <= dim <= MOE_NORM_MAX_DIM (else MOE_ERR_UNSUPPORTED), any dim without q; rows of
+ * dim % 8 == 0 elements on 16-byte aligned tensors take 16-byte accesses.  n, q and rstd's second
+ * half need w_pre; w_post, a gate and rstd's first half need y; at least one output is given.
+ * tokens == 0 returns MOE_OK.  Rows holding Inf or NaN give NaN in that row only. */
+moe_status_t moe_block_norm(const moe_block_norm_t *p, void *stream);
+
+typedef struct {
+  const void *dh;       /* [tokens, dim] as x: gradient of h, or NULL (zero); may be dx */
+  const uint16_t *dn;   /* [tokens, dim] bf16 gradient of n (of q's values too), or NULL (zero) */
+  void *dx;             /* out [tokens, dim] as x */
+  uint16_t *dy;         /* out [tokens, dim] bf16; given iff y is */
+  void *dgate;          /* out, type and shape of the gate; given iff there is a gate */
+  float *dw_post;       /* out [dim]; given iff w_post is */
+  float *dw_pre;        /* out [dim]; given iff dn is */
+} moe_block_norm_grads_t;
+
+/* Workspace of moe_block_norm_backward: one row of partial sums per workgroup for each of dw_pre,
+ * dw_post and a per-channel gate. */
+static inline size_t moe_block_norm_backward_ws_bytes(int32_t tokens, int32_t dim) {
+  size_t parts = tokens < MOE_NORM_PARTS ? ((size_t)(tokens > 0 ? tokens : 0) + 3) / 4 * 4 : MOE_NORM_PARTS;
+  return moe_align256(parts * 3 * (size_t)dim * 4);
+}
+
+/* moe_block_norm_backward -- gradients of moe_block_norm for its inputs, given those of h and n.
+ *   p         the forward call's struct: x, y, w_post, gate, w_pre, rstd (as the forward call wrote
+ *             it) and the options; h, n, q and q_scale are not read.  rstd is needed when w_post or
+ *             dn is given, w_pre when dn is.
+ * One of dh and dn is given.  Sums over tokens are added in a fixed order.  tokens == 0 sets the
+ * sums over tokens (dw_post, dw_pre, a per-channel dgate) to zero. */
+moe_status_t moe_block_norm_backward(const moe_block_norm_t *p, const moe_block_norm_grads_t *d, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* Most experts and most chosen experts of moe_router. */
+#define MOE_ROUTER_MAX_EXPERTS MOE_SORT_MAX_EXPERTS
+#define MOE_ROUTER_MAX_TOPK 32
+/* Waves per workgroup and most partial sums of the balance statistics. */
+#define MOE_ROUTER_WAVES 16
+#define MOE_ROUTER_PARTS 256
+
+typedef struct {
+  const void *logits;   /* [tokens, num_experts], bf16 or fp32 (dt) */
+  const float *bias;    /* [num_experts] added to the scores for the choice only, or NULL */
+  const uint8_t *valid; /* [tokens] 0 = leave the token out (padding), or NULL */
+  int32_t *topk_ids;    /* [tokens, topk]; written by moe_router, read by the backward pass */
+  float *topk_w;        /* [tokens, topk]; written by moe_router, not read by the backward pass */
+  int32_t tokens, num_experts, topk;
+  int32_t dt;           /* MOE_DT_BF16 or MOE_DT_F32 */
+  int32_t score;        /* moe_score_t */
+  int32_t renorm;       /* 1: the chosen weights are divided by their sum; 0: not */
+  float scale;          /* of the weights, finite */
+} moe_router_t;
+
+typedef struct {
+  float coef, z_coef;   /* of the balance loss and of the z loss, finite */
+  int32_t *counts;      /* [num_experts] how often each expert was chosen */
+  float *mean_prob;     /* [num_experts] mean probability over the counted tokens */
+  float *loss;          /* [2] balance loss, z loss */
+  int32_t *num_valid;   /* [1] counted tokens */
+} moe_balance_t;
+
+/* Workspace of moe_router with balance statistics (none without). */
+static inline size_t moe_router_ws_bytes(int32_t num_experts) {
+  return 512 + 8 * (size_t)MOE_ROUTER_PARTS + moe_align256((size_t)MOE_ROUTER_PARTS * (size_t)num_experts * 8);
+}
+
+/* moe_router -- the experts of each token and their weights, as moe_sort and moe_fused take them.
+ *     s = softmax(logits) or sigmoid(logits);   key = logits, or s + bias
+ *     topk_ids: the topk largest keys in descending order, equal keys by ascending expert
+ *     topk_w:   scale * s[id], with renorm divided by the sum of the chosen s
+ * The choice does not depend on rounding: keys with a bias are compared in 64 bits where fp32
+ * could not tell.  A logit of -inf or NaN, or a bias of -inf or NaN, masks its expert; +inf counts
+ * as the largest finite value, -0 as 0.  Slots left over (fewer than topk unmasked experts, an invalid
+ * token) get id -1 and weight 0; moe_sort skips them.
+ *   balance   or NULL: statistics of the batch, from the same pass over the logits.  Over the Tv
+ *             counted tokens (valid, with an unmasked logit), p = softmax(logits) or s / sum(s):
+ *             mean_prob = mean p; loss[0] = coef * sum_i counts_i * num_experts / (topk * Tv) * mean_prob_i;
+ *             loss[1] = z_coef * mean logsumexp(logits)^2.  Everything is 0 when Tv is.
+ *   ws        scratch of ws_bytes >= moe_router_ws_bytes(num_experts) with balance, else not read.
+ *             Needs no initial value; calls that overlap in time need one each.
+ * Limits: num_experts <= MOE_ROUTER_MAX_EXPERTS, topk <= min(num_experts, MOE_ROUTER_MAX_TOPK) (else
+ * MOE_ERR_UNSUPPORTED), tokens * num_experts < 2^40. */
+moe_status_t moe_router(const moe_router_t *r, const moe_balance_t *balance, void *ws, size_t ws_bytes, void *stream);
+
+/* moe_router_backward -- d_logits of the weights, the balance loss and the z loss.
+ *   r         as in the forward call, with topk_ids as it wrote them (ids outside [0, num_experts)
+ *             pass no gradient); bias and topk_w are not read: the choice itself has no gradient.
+ *   balance   or NULL: the forward call's struct; counts and num_valid are read (counts are
+ *             constants of the gradient), mean_prob and loss are not.
+ *   d_topk_w  [tokens, topk] gradient of topk_w, or NULL (zero).
+ *   d_loss    [2] on the device: gradients of the two losses, or NULL (ones).
+ *   d_logits  [tokens, num_experts] of type dt, overwritten; 0 for masked experts and left-out
+ *             tokens.  One of balance and d_topk_w is given. */
+moe_status_t moe_router_backward(const moe_router_t *r, const moe_balance_t *balance, const float *d_topk_w,
+                                 const float *d_loss, void *d_logits, void *stream);
+
+/* moe_quant_i8 -- symmetric 8-bit coding of bf16 rows, one fp32 scale per row.
+ *   x_bf16 [rows, cols], q_out int8 [rows, cols], scale_out [rows]; cols % 16 == 0, pointers to
+ *   rows 16-byte aligned (else MOE_ERR_INVALID_ARG).
+ * amax = max|x| of the row: scale = amax / 127, code = x * (127 / amax) rounded to nearest, ties
+ * to even.  A row with amax < 2^-100 has scale 0 and codes 0, a row holding Inf or NaN scale NaN
+ * and codes 0. */
+moe_status_t moe_quant_i8(const uint16_t *x_bf16, int64_t rows, int64_t cols, int8_t *q_out, float *scale_out,
+                          void *stream);
+
+/* Bytes of a packed weight row (in_features padded to 128) and of all of them (rows padded to 16). */
+static inline int64_t moe_i8_packed_k(int32_t in_features) { return ((int64_t)in_features + 127) / 128 * 128; }
+static inline size_t moe_i8_packed_bytes(int32_t out_features, int32_t in_features) {
+  return (size_t)((((int64_t)out_features + 15) / 16 * 16) * moe_i8_packed_k(in_features));
+}
+
+/* moe_pack_i8 -- reorder int8 weights [out_features, in_features] once into the layout moe_gemm_i8
+ * streams: 1 KB blocks (f, s) of rows 16 f .. 16 f + 15 and bytes 64 s .. 64 s + 63, s fastest; byte
+ * 16 (16 g + r) + b of a block is byte 64 s + 16 g + b of row 16 f + r; zero past the matrix.
+ * in_features % 16 == 0 and packed bytes < 2^32 (else MOE_ERR_UNSUPPORTED), both pointers 16-byte
+ * aligned, the byte ranges disjoint (else MOE_ERR_INVALID_ARG). */
+moe_status_t moe_pack_i8(const int8_t *w, int32_t out_features, int32_t in_features, int8_t *w_packed, void *stream);
+
+/* moe_gemm_i8 -- product of int8 tokens and packed int8 weights, exact in int32, scaled per token
+ * and per channel:
+ *     r[t, c] = a_scale[t] * w_scale[c] * sum_k a[t, k] * w[c, k]
+ *     out = r (+ add), or with act: out[t, i] = act(r[t, i], r[t, O/2 + i]) (+ add), O = out_features
+ *             (gate rows first, then the up rows, as w1 of moe_fused).
+ *   a         int8 [tokens, in_features], in_features % 16 == 0 and < 2^17 (else
+ *             MOE_ERR_UNSUPPORTED), 16-byte aligned; a_scale [tokens], w_scale [out_features] fp32.
+ *   act       or NULL; MOE_ACT_SITUV2 or MOE_ACT_SILU, then out_features % 32 == 0.
+ *   add       bf16, shape of out, or NULL; may be out.
+ *   out       bf16 [tokens, out_features], or [tokens, out_features / 2] with act; rounded once
+ *             from fp32.
+ * out_features >= 1, tokens * max(in_features, out_features) < 2^40, tokens < 2^24. */
+moe_status_t moe_gemm_i8(const int8_t *a, const float *a_scale, const int8_t *w_packed, const float *w_scale,
+                         int32_t tokens, int32_t out_features, int32_t in_features, const moe_act_params_t *act,
+                         const uint16_t *add, uint16_t *out_bf16, void *stream);
 
 /* The hipError_t value behind the last MOE_ERR_HIP returned on this thread (0 if none). */
 int32_t moe_last_hip_error(void);

@@ -5,6 +5,7 @@ their data pointers and torch's current stream are passed to the C entry points,
 step of the operator runs in the library's HIP kernels.  If the library is not built the
 calls raise; there is no fallback path.
 """
+import collections
 import ctypes
 import os
 
@@ -14,6 +15,7 @@ DT_BF16, DT_FP8, DT_FP4 = 0, 1, 2
 ACT_SITUV2, ACT_SILU, ACT_NONE_TEST = 0, 1, 2
 STAGE_1, STAGE_2, STAGE_ALL = 1, 2, 3
 W_ROW_MAJOR, W1_PACKED, W_PACKED = 0, 1, 2
+DT_F32, DT_I8 = 3, 4
 DTYPES = {"bf16": DT_BF16, "fp8": DT_FP8, "fp4": DT_FP4}
 ACTS = {"situv2": ACT_SITUV2, "silu": ACT_SILU, "none_test": ACT_NONE_TEST}
 
@@ -27,7 +29,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi35
 # the device and returns MOE_ERR_DEBUG_CHECK when a check failed)
 DEBUG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x_debug.so")
 EXPORTS = ("moe_sort", "moe_quant_act", "moe_pack_w1", "moe_pack_w2", "moe_fused", "moe_fused_noalloc",
-           "moe_last_hip_error")
+           "moe_block_norm", "moe_block_norm_backward", "moe_router", "moe_router_backward", "moe_quant_i8",
+           "moe_pack_i8", "moe_gemm_i8", "moe_last_hip_error")
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 
@@ -49,6 +52,27 @@ class Layout(ctypes.Structure):
 
 class ActParams(ctypes.Structure):
     _fields_ = [("act", ctypes.c_int32), ("beta", ctypes.c_float), ("linear_beta", ctypes.c_float)]
+
+
+class BlockNormParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "y", "w_post", "gate", "w_pre", "h", "n", "q", "q_scale", "rstd")]
+                + [(n, ctypes.c_int32) for n in ("tokens", "dim", "x_dt", "gate_kind", "gate_act", "q_dt")]
+                + [("scale", ctypes.c_float), ("eps", ctypes.c_float)])
+
+
+class BlockNormGradParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dh", "dn", "dx", "dy", "dgate", "dw_post", "dw_pre")]
+
+
+class RouterParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("logits", "bias", "valid", "topk_ids", "topk_w")]
+                + [(n, ctypes.c_int32) for n in ("tokens", "num_experts", "topk", "dt", "score", "renorm")]
+                + [("scale", ctypes.c_float)])
+
+
+class BalanceParams(ctypes.Structure):
+    _fields_ = ([("coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("counts", "mean_prob", "loss", "num_valid")])
 
 
 _lib = None
@@ -76,6 +100,21 @@ def lib():
         L.moe_pack_w1.restype = i32
         L.moe_pack_w2.argtypes = [vp, i32, i32, i32, vp, vp]
         L.moe_pack_w2.restype = i32
+        L.moe_block_norm.argtypes = [ctypes.POINTER(BlockNormParams), vp]
+        L.moe_block_norm.restype = i32
+        L.moe_block_norm_backward.argtypes = [ctypes.POINTER(BlockNormParams), ctypes.POINTER(BlockNormGradParams), vp,
+                                              sz, vp]
+        L.moe_block_norm_backward.restype = i32
+        L.moe_router.argtypes = [ctypes.POINTER(RouterParams), ctypes.POINTER(BalanceParams), vp, sz, vp]
+        L.moe_router.restype = i32
+        L.moe_router_backward.argtypes = [ctypes.POINTER(RouterParams), ctypes.POINTER(BalanceParams), vp, vp, vp, vp]
+        L.moe_router_backward.restype = i32
+        L.moe_quant_i8.argtypes = [vp, i64, i64, vp, vp, vp]
+        L.moe_quant_i8.restype = i32
+        L.moe_pack_i8.argtypes = [vp, i32, i32, vp, vp]
+        L.moe_pack_i8.restype = i32
+        L.moe_gemm_i8.argtypes = [vp, vp, vp, vp, i32, i32, i32, ctypes.POINTER(ActParams), vp, vp, vp]
+        L.moe_gemm_i8.restype = i32
         L.moe_last_hip_error.argtypes = []
         L.moe_last_hip_error.restype = i32
         _lib = L
@@ -301,4 +340,280 @@ def moe_fused_noalloc(x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, topk_w, l
                                                         _ptr(w1_scale), _ptr(w2), _ptr(w2_scale), _ptr(topk_w),
                                                         ctypes.byref(layout.c), T, K, num_local_experts, D, I,
                                                         ctypes.byref(params), _ptr(out), stages, _stream()))
+    return out
+
+
+# ------------------------------------------------------------------ around the routed experts
+#
+# These check their tensors (type, shape, dense rows, one device) before the C call checks the
+# rest, and run on the device of their first tensor, on torch's current stream of that device.
+
+NORM_MAX_DIM, NORM_PARTS = 16384, 512
+GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
+GATE_ACTS = {"none": 0, "sigmoid": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+ROUTER_MAX_TOPK, ROUTER_PARTS = 32, 256
+Q_DTYPES = {"fp8": DT_FP8, "fp4": DT_FP4, "i8": DT_I8}
+_ROW_TYPES = {torch.bfloat16: DT_BF16, torch.float32: DT_F32}
+
+BlockNorm = collections.namedtuple("BlockNorm", "h n q q_scale rstd")
+BlockNormGrads = collections.namedtuple("BlockNormGrads", "dx dy dgate dw_post dw_pre")
+Routing = collections.namedtuple("Routing", "ids w balance")
+Balance = collections.namedtuple("Balance", "counts mean_prob loss num_valid coef z_coef")
+
+
+def block_norm_backward_ws_bytes(tokens, dim):
+    return _align256((NORM_PARTS if tokens >= NORM_PARTS else (max(tokens, 0) + 3) // 4 * 4) * 3 * dim * 4)
+
+
+def router_ws_bytes(num_experts):
+    return 512 + 8 * ROUTER_PARTS + _align256(ROUTER_PARTS * num_experts * 8)
+
+
+def i8_packed_shape(out_features, in_features):
+    """Shape of moe_pack_i8's result: 1 KB blocks of 16 rows x 64 bytes."""
+    return ((out_features + 15) // 16, (in_features + 127) // 128 * 2, 1024)
+
+
+def _need(t, name, dtype, shape, device):
+    """The tensor's address (None for None), after its checks."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: need a dense {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{'a dense' if t.is_contiguous() else 'a strided'} {t.dtype} of {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _pick(table, key, name):
+    if key not in table:
+        raise ValueError(f"{name}: {key!r} is none of {', '.join(table)}")
+    return table[key]
+
+
+def _call(fn, device, *args):
+    """The library call on torch's current stream of `device`, with that device current."""
+    f = getattr(_lib or lib(), fn)
+    if device.index == torch.cuda.current_device():
+        status = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, torch.cuda.current_stream().cuda_stream)
+    if status:
+        _check(fn, status)
+
+
+def _on_gpu(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name}: need a tensor on the GPU, got one on {t.device}")
+    return t.device
+
+
+def _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, device):
+    if x.dim() != 2 or x.dtype not in _ROW_TYPES:
+        raise ValueError(f"x: need a bfloat16 or float32 tensor [tokens, dim], got {x.dtype} of {tuple(x.shape)}")
+    T, D = x.shape
+    kind = _pick(GATES, gate_kind, "gate_kind")
+    if (gate is None) != (kind == 0):
+        raise ValueError("gate and gate_kind go together")
+    p = BlockNormParams(tokens=T, dim=D, x_dt=_ROW_TYPES[x.dtype], gate_kind=kind,
+                        gate_act=_pick(GATE_ACTS, gate_act, "gate_act"), scale=scale, eps=eps)
+    p.x = _need(x, "x", x.dtype, (T, D), device)
+    p.y = _need(y, "y", torch.bfloat16, (T, D), device)
+    p.w_post = _need(w_post, "w_post", torch.float32, (D,), device)
+    p.w_pre = _need(w_pre, "w_pre", torch.float32, (D,), device)
+    if kind:
+        p.gate = _need(gate, "gate", torch.bfloat16 if kind == 3 else torch.float32,
+                       ((D,), (T,), (T, D))[kind - 1], device)
+    return p, T, D
+
+
+def moe_block_norm(x, y=None, *, w_post=None, gate=None, gate_kind="none", gate_act="none", scale=1.0, w_pre=None,
+                   eps=1e-6, h=None, want_n=True, q_dtype=None, stats=False):
+    """The norm after a block, its gate, the residual sum and the norm before the next block (see
+    moe_block_norm in the header).  x bf16 or fp32 [T, D], y bf16 [T, D], weights fp32 [D].
+
+    Returns BlockNorm(h, n, q, q_scale, rstd): h as x (None without y; pass h=x to update the stream in
+    place), n bf16 (None without w_pre or with want_n=False), q and q_scale for q_dtype "fp8", "fp4" or
+    "i8", rstd [2, T] with stats=True (the backward pass needs it)."""
+    device = _on_gpu(x, "x")
+    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, device)
+    n = q = q_scale = rstd = None
+    if h is not None:
+        p.h = _need(h, "h", x.dtype, (T, D), device)
+    elif y is not None:
+        h = torch.empty_like(x)
+        p.h = h.data_ptr()
+    if w_pre is not None and want_n:
+        n = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+        p.n = n.data_ptr()
+    if q_dtype is not None:
+        p.q_dt = _pick(Q_DTYPES, q_dtype, "q_dtype")
+        if w_pre is None:
+            raise ValueError("q_dtype: there is nothing to code without w_pre")
+        if p.q_dt == DT_I8:
+            q = torch.empty((T, D), dtype=torch.int8, device=device)
+            q_scale = torch.empty((T,), dtype=torch.float32, device=device)
+        else:
+            q = torch.empty((T, D if p.q_dt == DT_FP8 else D // 2), dtype=torch.uint8, device=device)
+            q_scale = torch.empty((T, D // 32), dtype=torch.uint8, device=device)
+        p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
+    if stats:
+        rstd = torch.empty((2, T), dtype=torch.float32, device=device)
+        p.rstd = rstd.data_ptr()
+    _call("moe_block_norm", device, p)
+    return BlockNorm(h, n, q, q_scale, rstd)
+
+
+def moe_block_norm_backward(x, y, rstd, dh, dn, *, w_post=None, gate=None, gate_kind="none", gate_act="none",
+                            scale=1.0, w_pre=None, ws=None):
+    """Gradients of moe_block_norm for its inputs, from those of h (dh, as x) and n (dn, bf16); either
+    may be None.  rstd: as moe_block_norm(stats=True) returned it; the other arguments as given there.
+    Returns BlockNormGrads(dx, dy, dgate, dw_post, dw_pre), None for what was not given."""
+    device = _on_gpu(x, "x")
+    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, 1.0, device)
+    p.rstd = _need(rstd, "rstd", torch.float32, (2, T), device)
+    g = BlockNormGradParams()
+    g.dh = _need(dh, "dh", x.dtype, (T, D), device)
+    g.dn = _need(dn, "dn", torch.bfloat16, (T, D), device)
+    dx, dy, dgate, dw_post, dw_pre = torch.empty_like(x), None, None, None, None
+    g.dx = dx.data_ptr()
+    if y is not None:
+        dy = torch.empty_like(y)
+        g.dy = dy.data_ptr()
+    if gate is not None:
+        dgate = torch.empty_like(gate)
+        g.dgate = dgate.data_ptr()
+    if w_post is not None:
+        dw_post = torch.empty_like(w_post)
+        g.dw_post = dw_post.data_ptr()
+    if dn is not None:
+        dw_pre = torch.empty((D,), dtype=torch.float32, device=device)
+        g.dw_pre = dw_pre.data_ptr()
+    if ws is None:
+        ws = torch.empty(block_norm_backward_ws_bytes(T, D), dtype=torch.uint8, device=device)
+    _call("moe_block_norm_backward", device, p, g, _need(ws, "ws", torch.uint8, ws.shape, device), ws.numel())
+    return BlockNormGrads(dx, dy, dgate, dw_post, dw_pre)
+
+
+def _router_params(logits, topk, score, renorm, scale, bias, valid, device):
+    if logits.dim() != 2 or logits.dtype not in _ROW_TYPES:
+        raise ValueError(f"logits: need a bfloat16 or float32 tensor [tokens, experts], got {logits.dtype} of "
+                         f"{tuple(logits.shape)}")
+    T, E = logits.shape
+    if valid is not None and valid.dtype == torch.bool:
+        valid = valid.view(torch.uint8)
+    r = RouterParams(tokens=T, num_experts=E, topk=topk, dt=_ROW_TYPES[logits.dtype],
+                     score=_pick(SCORES, score, "score"), renorm=int(bool(renorm)), scale=scale)
+    r.logits = _need(logits, "logits", logits.dtype, (T, E), device)
+    r.bias = _need(bias, "bias", torch.float32, (E,), device)
+    r.valid = _need(valid, "valid", torch.uint8, (T,), device)
+    return r, T, E
+
+
+def moe_router(logits, topk, *, score="softmax", renorm=True, scale=1.0, bias=None, valid=None, balance=None, ws=None):
+    """The topk experts of each token and their weights, as moe_sort and moe_fused take them (see
+    moe_router in the header).  logits bf16 or fp32 [T, E]; bias fp32 [E], for the choice only; valid
+    bool or uint8 [T], 0 for padding; balance: (coef, z_coef) to take the balance loss, the z loss and
+    the per-expert counts in the same pass.
+
+    Returns Routing(ids int32 [T, topk], w fp32 [T, topk], balance), balance being None or
+    Balance(counts, mean_prob, loss [2], num_valid, coef, z_coef)."""
+    device = _on_gpu(logits, "logits")
+    r, T, E = _router_params(logits, topk, score, renorm, scale, bias, valid, device)
+    ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=device)
+    w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=device)
+    r.topk_ids, r.topk_w = ids.data_ptr(), w.data_ptr()
+    if balance is None:
+        _call("moe_router", device, r, None, None, 0)
+        return Routing(ids, w, None)
+    coef, z_coef = balance
+    b = Balance(torch.empty((E,), dtype=torch.int32, device=device), torch.empty((E,), dtype=torch.float32, device=device),
+                torch.empty((2,), dtype=torch.float32, device=device), torch.empty((1,), dtype=torch.int32, device=device),
+                coef, z_coef)
+    if ws is None:
+        ws = torch.empty(router_ws_bytes(E), dtype=torch.uint8, device=device)
+    _call("moe_router", device, r, _balance_params(b), _need(ws, "ws", torch.uint8, ws.shape, device), ws.numel())
+    return Routing(ids, w, b)
+
+
+def _balance_params(b):
+    return BalanceParams(b.coef, b.z_coef, b.counts.data_ptr(), b.mean_prob.data_ptr(), b.loss.data_ptr(),
+                         b.num_valid.data_ptr())
+
+
+def moe_router_backward(logits, routing, d_w=None, *, d_loss=None, score="softmax", renorm=True, scale=1.0, valid=None):
+    """d_logits of moe_router, given its result: from d_w (fp32 [T, topk], gradient of the weights) and,
+    where it took the balance statistics, d_loss (fp32 [2] on the GPU, gradients of the two losses;
+    None for ones).  The other arguments as in the forward call."""
+    device = _on_gpu(logits, "logits")
+    if routing.ids.dim() != 2:
+        raise ValueError(f"routing.ids: need [tokens, topk], got {tuple(routing.ids.shape)}")
+    topk = routing.ids.shape[1]
+    r, T, E = _router_params(logits, topk, score, renorm, scale, None, valid, device)
+    r.topk_ids = _need(routing.ids, "routing.ids", torch.int32, (T, topk), device)
+    b = routing.balance
+    if b is not None:
+        _need(b.counts, "balance.counts", torch.int32, (E,), device)
+        _need(b.num_valid, "balance.num_valid", torch.int32, (1,), device)
+        b = _balance_params(b)
+    d_logits = torch.empty_like(logits)
+    _call("moe_router_backward", device, r, b, _need(d_w, "d_w", torch.float32, (T, topk), device),
+          _need(d_loss, "d_loss", torch.float32, (2,), device), d_logits.data_ptr())
+    return d_logits
+
+
+def moe_quant_i8(x, q=None, scale=None):
+    """bf16 [rows, cols] -> (int8 codes, fp32 scale per row), see moe_quant_i8 in the header."""
+    device = _on_gpu(x, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x: need [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    if scale is None:
+        scale = torch.empty((rows,), dtype=torch.float32, device=device)
+    _call("moe_quant_i8", device, _need(x, "x", torch.bfloat16, (rows, cols), device), rows, cols,
+          _need(q, "q", torch.int8, (rows, cols), device), _need(scale, "scale", torch.float32, (rows,), device))
+    return q, scale
+
+
+def moe_pack_i8(w, out=None):
+    """int8 weights [out_features, in_features] -> the packed layout moe_gemm_i8 reads."""
+    device = _on_gpu(w, "w")
+    if w.dim() != 2:
+        raise ValueError(f"w: need [out_features, in_features], got {tuple(w.shape)}")
+    N, K = w.shape
+    shape = i8_packed_shape(N, K)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int8, device=device)
+    _call("moe_pack_i8", device, _need(w, "w", torch.int8, (N, K), device), N, K,
+          _need(out, "out", torch.int8, shape, device))
+    return out
+
+
+def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_beta=None, add=None, out=None):
+    """int8 tokens [T, K] (scales [T]) times packed int8 weights of w_scale.numel() rows -> bf16, with
+    act "situv2" or "silu" of the [gate|up] halves and `add` (bf16, shape of the result) in the same
+    launch (see moe_gemm_i8 in the header)."""
+    device = _on_gpu(a, "a")
+    if a.dim() != 2 or w_scale.dim() != 1:
+        raise ValueError(f"need a [tokens, in_features] and w_scale [out_features], got {tuple(a.shape)} and "
+                         f"{tuple(w_scale.shape)}")
+    T, K = a.shape
+    N = w_scale.shape[0]
+    params = None
+    if act is not None:
+        k = _pick(ACTS, act, "act")
+        if k == ACT_SITUV2 and (beta is None or linear_beta is None):
+            raise ValueError("SiTUv2 needs beta and linear_beta (there are no defaults)")
+        params = ActParams(k, 0.0 if beta is None else beta, 0.0 if linear_beta is None else linear_beta)
+    shape = (T, N if act is None else N // 2)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _call("moe_gemm_i8", device, _need(a, "a", torch.int8, (T, K), device),
+          _need(a_scale, "a_scale", torch.float32, (T,), device),
+          _need(w_packed, "w_packed", torch.int8, i8_packed_shape(N, K), device),
+          _need(w_scale, "w_scale", torch.float32, (N,), device), T, N, K, params,
+          _need(add, "add", torch.bfloat16, shape, device), _need(out, "out", torch.bfloat16, shape, device))
     return out

@@ -279,3 +279,168 @@ moe_status_t moe_fused_noalloc(const void* x, const uint8_t* x_scale, int32_t a_
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- around the routed experts
+
+namespace {
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool row_type(int32_t dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_F32; }
+
+// What the forward and the backward pass of the block norm both require; *a is filled.
+moe_status_t check_norm(const moe_block_norm_t* p, moe::NormArgs* a) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->dim <= 0 || !row_type(p->x_dt)) return MOE_ERR_INVALID_ARG;
+  if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
+  if (p->gate_act != MOE_GATE_RAW && p->gate_act != MOE_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (p->gate_kind == MOE_GATE_NONE && p->gate_act != MOE_GATE_RAW) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || !std::isfinite(p->eps) || p->eps <= 0.f) return MOE_ERR_INVALID_ARG;
+  if ((p->gate_kind == MOE_GATE_NONE) != (p->gate == nullptr) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
+  if (!p->y && (p->w_post || p->gate_kind != MOE_GATE_NONE) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
+  if (p->dim > MOE_NORM_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+  if (p->tokens > 0 && !p->x) return MOE_ERR_INVALID_ARG;
+  *a = moe::NormArgs{p->x, p->y, p->w_post, p->gate, p->w_pre, p->h, p->n, p->q, p->q_scale, p->rstd,
+                     p->tokens, p->dim, p->x_dt, p->gate_kind, p->gate_act, p->q_dt, p->scale, p->eps};
+  return MOE_OK;
+}
+
+moe_status_t check_router(const moe_router_t* r, const moe_balance_t* b, moe::RouterArgs* a, moe::BalanceArgs* ba) {
+  if (!r) return MOE_ERR_INVALID_ARG;
+  if (r->tokens < 0 || r->num_experts < 1 || r->topk < 1 || !row_type(r->dt)) return MOE_ERR_INVALID_ARG;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if ((r->renorm != 0 && r->renorm != 1) || !std::isfinite(r->scale)) return MOE_ERR_INVALID_ARG;
+  if (b && (!std::isfinite(b->coef) || !std::isfinite(b->z_coef))) return MOE_ERR_INVALID_ARG;
+  if (r->num_experts > MOE_ROUTER_MAX_EXPERTS || r->topk > MOE_ROUTER_MAX_TOPK || r->topk > r->num_experts)
+    return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)r->tokens * r->num_experts >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (r->tokens > 0 && !r->logits) return MOE_ERR_INVALID_ARG;
+  *a = moe::RouterArgs{r->logits, r->bias, r->valid, r->topk_ids, r->topk_w, r->tokens, r->num_experts, r->topk,
+                       r->dt, r->score, r->renorm, r->scale};
+  if (b) *ba = moe::BalanceArgs{b->coef, b->z_coef, b->counts, b->mean_prob, b->loss, b->num_valid};
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_block_norm(const moe_block_norm_t* p, void* stream) {
+  moe::NormArgs a;
+  const moe_status_t st = check_norm(p, &a);
+  if (st != MOE_OK) return st;
+  if ((p->q == nullptr) != (p->q_scale == nullptr) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
+  if (p->q) {
+    if (p->q_dt != MOE_DT_FP8_E4M3 && p->q_dt != MOE_DT_FP4_E2M1 && p->q_dt != MOE_DT_I8) return MOE_ERR_INVALID_ARG;
+    if (p->dim % (p->q_dt == MOE_DT_I8 ? 16 : 32) != 0) return MOE_ERR_UNSUPPORTED;
+  }
+  if (p->tokens == 0) return MOE_OK;
+  if ((p->n || p->q) && !p->w_pre) return MOE_ERR_INVALID_ARG;
+  if (!p->h && !p->n && !p->q) return MOE_ERR_INVALID_ARG;
+  const bool shared_gate = p->gate_kind == MOE_GATE_TOKEN;
+  if (p->q && !(aligned16(p->x) && aligned16(p->y) && aligned16(p->w_post) && (shared_gate || aligned16(p->gate)) &&
+                aligned16(p->w_pre) && aligned16(p->h) && aligned16(p->n) && aligned16(p->q)))
+    return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_block_norm(a, (hipStream_t)stream)));
+}
+
+moe_status_t moe_block_norm_backward(const moe_block_norm_t* p, const moe_block_norm_grads_t* d, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  moe::NormBackwardArgs b;
+  const moe_status_t st = check_norm(p, &b.f);
+  if (st != MOE_OK) return st;
+  if (!d) return MOE_ERR_INVALID_ARG;
+  const bool some = p->tokens > 0;
+  if (some && !d->dh && !d->dn) return MOE_ERR_INVALID_ARG;
+  if (some && (!d->dx || (d->dy == nullptr) != (p->y == nullptr))) return MOE_ERR_INVALID_ARG;
+  if (some && (d->dgate == nullptr) != (p->gate_kind == MOE_GATE_NONE)) return MOE_ERR_INVALID_ARG;
+  if ((d->dw_post == nullptr) != (p->w_post == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (some && (d->dw_pre == nullptr) != (d->dn == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (d->dn && !p->w_pre) return MOE_ERR_INVALID_ARG;
+  if (some && (p->w_post || d->dn) && !p->rstd) return MOE_ERR_INVALID_ARG;
+  if (some && !ws) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_block_norm_backward_ws_bytes(p->tokens, p->dim)) return MOE_ERR_WORKSPACE;
+  b.dh = d->dh;
+  b.dn = d->dn;
+  b.dx = d->dx;
+  b.dy = d->dy;
+  b.dgate = d->dgate;
+  b.dw_post = d->dw_post;
+  b.dw_pre = d->dw_pre;
+  b.part = (float*)ws;
+  return finish(hip_status(moe::launch_block_norm_backward(b, (hipStream_t)stream)));
+}
+
+moe_status_t moe_router(const moe_router_t* r, const moe_balance_t* balance, void* ws, size_t ws_bytes, void* stream) {
+  moe::RouterArgs a;
+  moe::BalanceArgs b;
+  const moe_status_t st = check_router(r, balance, &a, &b);
+  if (st != MOE_OK) return st;
+  if (r->tokens > 0 && (!r->topk_ids || !r->topk_w)) return MOE_ERR_INVALID_ARG;
+  if (balance) {
+    if (!b.counts || !b.mean_prob || !b.loss || !b.num_valid || !ws) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe_router_ws_bytes(r->num_experts)) return MOE_ERR_WORKSPACE;
+  } else if (r->tokens == 0) {
+    return MOE_OK;
+  }
+  return finish(hip_status(moe::launch_router(a, balance ? &b : nullptr, ws, (hipStream_t)stream)));
+}
+
+moe_status_t moe_router_backward(const moe_router_t* r, const moe_balance_t* balance, const float* d_topk_w,
+                                 const float* d_loss, void* d_logits, void* stream) {
+  moe::RouterArgs a;
+  moe::BalanceArgs b;
+  const moe_status_t st = check_router(r, balance, &a, &b);
+  if (st != MOE_OK) return st;
+  if (r->tokens == 0) return MOE_OK;
+  if (!d_logits || (!balance && !d_topk_w)) return MOE_ERR_INVALID_ARG;
+  if (d_topk_w && !r->topk_ids) return MOE_ERR_INVALID_ARG;
+  if (balance && (!b.counts || !b.num_valid)) return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_router_backward(a, balance ? &b : nullptr, d_topk_w, d_loss, d_logits,
+                                                       (hipStream_t)stream)));
+}
+
+moe_status_t moe_quant_i8(const uint16_t* x_bf16, int64_t rows, int64_t cols, int8_t* q_out, float* scale_out,
+                          void* stream) {
+  if (rows < 0 || cols <= 0 || cols % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x_bf16 || !q_out || !scale_out || !aligned16(x_bf16) || !aligned16(q_out)) return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_quant_i8(x_bf16, rows, cols, (uint8_t*)q_out, scale_out, (hipStream_t)stream)));
+}
+
+moe_status_t moe_pack_i8(const int8_t* w, int32_t out_features, int32_t in_features, int8_t* w_packed, void* stream) {
+  if (!w || !w_packed || out_features < 1 || in_features < 1 || !aligned16(w) || !aligned16(w_packed))
+    return MOE_ERR_INVALID_ARG;
+  const size_t packed = moe_i8_packed_bytes(out_features, in_features);
+  if (in_features % 16 != 0 || packed >= ((size_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  const uintptr_t a = (uintptr_t)w, b = (uintptr_t)w_packed;
+  if (a < b + packed && b < a + (uintptr_t)out_features * (uintptr_t)in_features) return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_pack_i8((const uint8_t*)w, out_features, in_features, (uint8_t*)w_packed,
+                                               (hipStream_t)stream)));
+}
+
+moe_status_t moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* w_packed, const float* w_scale,
+                         int32_t tokens, int32_t out_features, int32_t in_features, const moe_act_params_t* act,
+                         const uint16_t* add, uint16_t* out_bf16, void* stream) {
+  if (tokens < 0 || out_features < 1 || in_features < 1) return MOE_ERR_INVALID_ARG;
+  if (act) {
+    if (act->act != MOE_ACT_SITUV2 && act->act != MOE_ACT_SILU) return MOE_ERR_UNSUPPORTED;
+    if (act->act == MOE_ACT_SITUV2 &&
+        !(std::isfinite(act->beta) && act->beta > 0.f && std::isfinite(act->linear_beta) && act->linear_beta > 0.f))
+      return MOE_ERR_INVALID_ARG;
+    if (out_features % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  }
+  if (in_features % 16 != 0 || in_features >= (1 << 17) || tokens >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (moe_i8_packed_bytes(out_features, in_features) >= ((size_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  const int32_t wider = in_features > out_features ? in_features : out_features;
+  if ((int64_t)tokens * wider >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (tokens == 0) return MOE_OK;
+  if (!a || !a_scale || !w_packed || !w_scale || !out_bf16 || !aligned16(a) || !aligned16(w_packed))
+    return MOE_ERR_INVALID_ARG;
+  const moe::GemmI8Args g{(const uint8_t*)a, a_scale, (const uint8_t*)w_packed, w_scale, add, out_bf16, tokens,
+                          out_features, in_features, act ? act->act : -1, act ? act->beta : 0.f,
+                          act ? act->linear_beta : 0.f};
+  return finish(hip_status(moe::launch_gemm_i8(g, (hipStream_t)stream)));
+}
+
+}  // extern "C"

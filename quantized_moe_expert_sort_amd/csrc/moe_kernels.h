@@ -122,6 +122,71 @@ hipError_t launch_pack_w2(const uint8_t* w2, uint8_t* out, int E, int D, int I, 
 // workgroups signal each other through the layout's sync words.
 hipError_t launch_single(const FusedArgs& a, hipStream_t s);
 
+// Block norms (moe_norm.hip).  Pointers and options as in moe_block_norm_t; null = not given.
+struct NormArgs {
+  const void* x;           // [T, D] bf16 or fp32
+  const uint16_t* y;       // [T, D] bf16 or null
+  const float* w_post;     // [D] or null
+  const void* gate;        // by gate_kind
+  const float* w_pre;      // [D] or null
+  void* h;                 // [T, D] as x, or null
+  uint16_t* n;             // [T, D] bf16 or null
+  void* q;                 // codes or null
+  void* q_scale;
+  float* rstd;             // [2, T] or null
+  int T, D, x_dt, gate_kind, gate_act, q_dt;
+  float scale, eps;
+};
+struct NormBackwardArgs {
+  NormArgs f;              // x, y, w_post, gate, w_pre, rstd and the options of the forward call
+  const void* dh;          // [T, D] as x, or null
+  const uint16_t* dn;      // [T, D] bf16 or null
+  void* dx;                // [T, D] as x
+  uint16_t* dy;            // [T, D] bf16 or null
+  void* dgate;             // by gate_kind
+  float* dw_post;          // [D] or null
+  float* dw_pre;           // [D] or null
+  float* part;             // [MOE_NORM_PARTS, 3, D] partial sums
+};
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
+hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s);
+
+// Router and balance loss (moe_router.hip), as moe_router_t and moe_balance_t.
+struct RouterArgs {
+  const void* logits;      // [T, E] bf16 or fp32
+  const float* bias;       // [E] or null
+  const uint8_t* valid;    // [T] or null
+  int32_t* ids;            // [T, K]
+  float* w;                // [T, K] (forward)
+  int T, E, K, dt, score, renorm;
+  float scale;
+};
+struct BalanceArgs {
+  float coef, z_coef;
+  int32_t* counts;         // [E]
+  float* mean_prob;        // [E]
+  float* loss;             // [2]
+  int32_t* num_valid;      // [1]
+};
+hipError_t launch_router(const RouterArgs& a, const BalanceArgs* b, void* ws, hipStream_t s);
+hipError_t launch_router_backward(const RouterArgs& a, const BalanceArgs* b, const float* dw, const float* dloss,
+                                  void* dlogits, hipStream_t s);
+
+// Products in 8-bit integers (moe_int8.hip).
+struct GemmI8Args {
+  const uint8_t* a;        // [T, K] int8
+  const float* sa;         // [T]
+  const uint8_t* w;        // packed by launch_pack_i8
+  const float* sw;         // [N]
+  const uint16_t* add;     // [T, No] bf16 or null
+  uint16_t* out;           // [T, No] bf16
+  int T, N, K, act;        // act < 0: none, No = N; else No = N / 2
+  float beta, linear_beta;
+};
+hipError_t launch_quant_i8(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q, float* scale, hipStream_t s);
+hipError_t launch_pack_i8(const uint8_t* w, int N, int K, uint8_t* out, hipStream_t s);
+hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t s);
+
 // Word offsets inside the sync array.  Every counter has a 64-byte line of its own: device-scope
 // atomics on one line are serialized (about 11 ns each on gfx950), whatever word they touch.
 //   line 0               word 0: sticky timeout flag

@@ -1,0 +1,661 @@
+// Router: scores of a token's experts, the K chosen ones and their weights (what moe_sort and
+// moe_fused read), with the balance loss, the z loss and the per-expert counts of the batch taken
+// in the same pass over the logits; and the gradient of all of it for the logits.
+//
+// Row t, expert i:  s = softmax(l) or sigmoid(l);  key = l, or s + bias;  the K largest keys in
+// descending order, equal keys by ascending expert;  w = scale s (/ sum of the chosen s).
+//   p = softmax(l), or s / sum(s);  P_i = mean_t p_ti;  c_i = how often i was chosen;
+//   loss[0] = coef sum_i (c_i E / (K Tv)) P_i;  loss[1] = z_coef mean_t logsumexp(l_t)^2
+// over the Tv counted rows.  A logit of -inf or NaN masks its expert, +inf counts as the largest
+// finite value; a row whose logits are all masked, or that `valid` leaves out, chooses nothing
+// (ids -1, weights 0) and is not counted.
+//
+// One wave takes a row; each lane keeps up to 32 logits in registers, so the row is read once.
+// Choosing K of E: a bound that at least K keys reach is found among the 64 lane maxima (a search
+// over the bits of the key, one ballot a bit), the keys at or above it (K to K + a few of 896)
+// are compacted to one per lane through LDS, and every lane counts how many of them come before
+// its own.  K rounds of a maximum over the wave would take about 4 times the instructions at
+// E 896, K 16; they remain for rows where more than 64 keys reach the bound (long runs of equal
+// keys).  With a bias the keys are sums whose order could depend on rounding, so the compacted
+// candidates (taken with a margin for the fp32 error) are ranked by keys in 64 bits.
+//
+// Bound by the bytes of the logits in the backward pass, by instructions in the forward one.
+#include "moe_kernels.h"
+#include "moe_rows.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float BIG = 3.402823466e38f;
+constexpr int CAND = 64;                      // candidates of a row, at most one per lane
+constexpr int HAND = 4;                       // rows of LDS in which waves hand over their sums
+
+// LDS written by some lanes of a wave is read by others of the same wave after this.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * LOG2E); }
+
+// sigmoid(x) e^-m for m <= 0: with m the smaller of 0 and the largest logit, quotients of sigmoids do
+// not underflow however negative all of them are.
+__device__ __forceinline__ float sigmoid_over(float x, float m) {
+  return exp_f(__builtin_fminf(x, 0.0f) - m) * __builtin_amdgcn_rcpf(1.0f + exp_f(-__builtin_fabsf(x)));
+}
+
+// The order of the keys as unsigned integers; 0 is left for masked experts.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);               // -0 and +0 are equal keys
+  return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Column of a lane's register i: chunks of 64 * VEC columns, VEC consecutive ones per lane.
+template <int VEC>
+__device__ __forceinline__ int column(int i, int lane) { return ((i / VEC) * 64 + lane) * VEC + i % VEC; }
+
+// A row's logits, masked ones (and columns past E) as -inf.
+template <class LT, int VEC, int NREG>
+__device__ __forceinline__ void load_logits(const LT* row, int E, int lane, float (&l)[NREG]) {
+#pragma unroll
+  for (int c = 0; c < NREG / VEC; ++c) {
+    float v[VEC];
+    const int col = (c * 64 + lane) * VEC;
+    if (col < E) {                                            // E % VEC == 0
+      load_row<VEC>(row + col, v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) l[c * VEC + j] = v[j] > -INFINITY ? __builtin_fminf(v[j], BIG) : -INFINITY;
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) l[c * VEC + j] = -INFINITY;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, WAVE);
+  return v;
+}
+__device__ __forceinline__ float readlane_f(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ double readlane_d(double v, int l) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), l), __builtin_amdgcn_readlane(__double2loint(v), l));
+}
+
+// The selection key in 64 bits.  m, zd: the row's largest logit and sum of exp(l - m) (softmax).
+__device__ __forceinline__ double exact_key(float l, float bias, int score, float m, double zd) {
+  const double x = (double)l;
+  const double s = score == MOE_SCORE_SOFTMAX ? exp(x - (double)m) / zd
+                   : x >= 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x) / (1.0 + exp(x));
+  return s + (double)bias;
+}
+
+// One wave's row: on return lane r < *chosen holds the expert of rank r (ascending rank), its
+// logit, and -1 / -inf from there on.  cand: CAND entries of this wave.
+template <int VEC, int NREG, bool BIAS>
+__device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias, int E, int K, int score, float m,
+                                       float z, uint2* cand, int lane, int& id, float& logit) {
+  id = -1;
+  logit = -INFINITY;
+  uint32_t key[NREG];
+  uint32_t best = 0;
+#pragma unroll
+  for (int i = 0; i < NREG; ++i) {
+    if constexpr (BIAS) {
+      const int col = column<VEC>(i, lane);
+      const float b = col < E ? bias[col] : 0.0f;
+      const float s = score == MOE_SCORE_SOFTMAX ? exp_f(l[i] - m) / z : fast_sigmoid(l[i]);
+      key[i] = l[i] > -INFINITY && b > -INFINITY ? ordered(s + __builtin_fminf(b, BIG)) : 0u;
+    } else {
+      key[i] = l[i] > -INFINITY ? ordered(l[i]) : 0u;
+    }
+    best = max(best, key[i]);
+  }
+  // a bound that at least K lane maxima reach (0 if fewer than K lanes have one)
+  uint32_t bound = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t t = bound | (1u << bit);
+    const int n = __popcll(__ballot(best >= t));
+    if (n >= K) {
+      bound = t;
+      if (n <= K + 2) break;
+    }
+  }
+  float margin = 0.0f;
+  if constexpr (BIAS) {
+    // The fp32 keys are off by less than margin / 2: a score by 4e-6 at most (the rounding of the
+    // exponents, of the sum of up to 2048 exponentials and of the quotient), the sum of score and
+    // bias by 2^-24 of itself.  So every expert among the K largest exact keys has an fp32 key of
+    // at least bound - margin.
+    const float b = bound ? unordered(bound) : 0.0f;
+    margin = 1e-5f * (1.0f + __builtin_fabsf(b));
+    if (bound) bound = max(ordered(__builtin_fmaxf(b - margin, -BIG)), 1u);
+  }
+  bound = max(bound, 1u);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NREG; ++i) {
+    const uint64_t mask = __ballot(key[i] >= bound);
+    if (mask) {
+      if (key[i] >= bound) {
+        const int p = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (p < CAND) cand[p] = uint2{__float_as_uint(l[i]), (uint32_t)column<VEC>(i, lane)};
+      }
+      n += __popcll(mask);
+    }
+  }
+  wave_sync();
+  double zd = 1.0;
+  const auto exact_z = [&]() {
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < NREG; ++i)
+      if (l[i] > -INFINITY) s += exp((double)l[i] - (double)m);
+    zd = wave_sum_f64(s);
+  };
+  if (n <= CAND) {
+    const bool have = lane < n;
+    const uint2 c = have ? cand[lane] : uint2{0xFF800000u, 0x7FFFFFFFu};
+    const float cl = __uint_as_float(c.x);
+    int rank = 0;
+    if constexpr (BIAS) {
+      const float b = have ? __builtin_fminf(bias[c.y], BIG) : 0.0f;
+      double k = 0.0;
+      bool done = false;
+      if (score == MOE_SCORE_SOFTMAX) {
+        // fp32 keys decide unless two of them are close: the sum in 64 bits costs more than the rest
+        const float k32 = exp_f(cl - m) / z + b;
+        bool close = false;
+        for (int j = 0; j < n; ++j) {
+          const float o = readlane_f(k32, j);
+          rank += o > k32;
+          close |= j != lane && __builtin_fabsf(o - k32) <= 1e-5f * (1.0f + __builtin_fabsf(k32));
+        }
+        done = __ballot(have && close) == 0;
+        if (!done) exact_z();
+      }
+      if (!done) {
+        rank = 0;
+        if (have) k = exact_key(cl, b, score, m, zd);
+        for (int j = 0; j < n; ++j) {
+          const double o = readlane_d(k, j);
+          const int oc = __builtin_amdgcn_readlane((int)c.y, j);
+          rank += o > k || (o == k && oc < (int)c.y);
+        }
+      }
+    } else {
+      const uint32_t k = ordered(cl);
+      for (int j = 0; j < n; ++j) {
+        const uint32_t o = __builtin_amdgcn_readlane(k, j);
+        const int oc = __builtin_amdgcn_readlane((int)c.y, j);
+        rank += o > k || (o == k && oc < (int)c.y);
+      }
+    }
+    // to the lane of its rank (ranks of the candidates are 0 .. n - 1, each once)
+    wave_sync();
+    if (have) cand[rank] = c;
+    wave_sync();
+    if (lane < min(n, K)) {
+      const uint2 r = cand[lane];
+      id = (int)r.y;
+      logit = __uint_as_float(r.x);
+    }
+    wave_sync();
+    return;
+  }
+  // more than 64 candidates: K maxima, each over every key that is left
+  if constexpr (BIAS)
+    if (score == MOE_SCORE_SOFTMAX) exact_z();
+  uint32_t taken = 0;
+  for (int r = 0; r < K; ++r) {
+    double bk = -INFINITY;
+    int bc = 0x7FFFFFFF, bi = -1;
+    float bl = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) {
+      if (key[i] >= bound && !((taken >> i) & 1)) {
+        const int col = column<VEC>(i, lane);
+        double k;
+        if constexpr (BIAS) k = exact_key(l[i], __builtin_fminf(bias[col], BIG), score, m, zd);
+        else k = (double)l[i];
+        if (bi < 0 || k > bk) { bk = k; bc = col; bi = i; bl = l[i]; }   // columns ascend with i
+      }
+    }
+    double wk = bk;
+    int wc = bc;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const double ok = __shfl_xor(wk, d, WAVE);
+      const int oc = __shfl_xor(wc, d, WAVE);
+      if (ok > wk || (ok == wk && oc < wc)) { wk = ok; wc = oc; }
+    }
+    const bool mine = bi >= 0 && bc == wc;                    // columns are distinct: one lane
+    if (mine) taken |= 1u << bi;
+    const uint64_t who = __ballot(mine);
+    if (!who) break;
+    const float wl = readlane_f(bl, __ffsll((unsigned long long)who) - 1);
+    if (lane == r) { id = wc; logit = wl; }
+  }
+}
+
+// ws of the balance statistics: [256] a ticket, [parts] Tv, [parts] z sums, [ceil(E / 64)] loss
+// parts, then counts [parts, E] and probability sums [parts, E].
+struct BalanceParts {
+  int32_t* ticket;
+  int32_t* tv;
+  float* z;
+  float* loss;
+  int32_t* counts;
+  float* psum;
+};
+__host__ __device__ inline BalanceParts balance_parts(void* ws, int E) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  BalanceParts b;
+  b.ticket = reinterpret_cast<int32_t*>(p);
+  b.tv = reinterpret_cast<int32_t*>(p + 256);
+  b.z = reinterpret_cast<float*>(p + 256 + 4 * MOE_ROUTER_PARTS);
+  b.loss = reinterpret_cast<float*>(p + 256 + 8 * MOE_ROUTER_PARTS);
+  b.counts = reinterpret_cast<int32_t*>(p + 256 + 8 * MOE_ROUTER_PARTS + 256);
+  b.psum = reinterpret_cast<float*>(b.counts + (size_t)MOE_ROUTER_PARTS * E);
+  return b;
+}
+
+// Rows wave, wave + waves of the grid, ...
+template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
+__global__ __launch_bounds__(BAL ? MOE_ROUTER_WAVES * 64 : 256) void router_kernel(const RouterArgs a, void* ws) {
+  extern __shared__ uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  uint2* const cand = reinterpret_cast<uint2*>(lds) + wave * CAND;
+  int32_t* const hist = reinterpret_cast<int32_t*>(lds + (size_t)waves * CAND * sizeof(uint2));   // BAL: [E]
+  float* const handed = reinterpret_cast<float*>(hist + a.E);                                     // BAL: [HAND, E]
+  float psum[BAL ? NREG : 1];
+  float zsum = 0.0f;
+  int tv = 0;
+  if constexpr (BAL) {
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) psum[i] = 0.0f;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) hist[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *balance_parts(ws, a.E).ticket = 0;
+    __syncthreads();
+  }
+  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves) {
+    int id = -1;
+    float w = 0.0f;
+    if (!a.valid || a.valid[t]) {
+      float l[NREG];
+      load_logits<LT, VEC, NREG>(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane, l);
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NREG; ++i) m = __builtin_fmaxf(m, l[i]);
+      m = wave_max(m);
+      if (m > -INFINITY) {
+        float z = 1.0f;
+        if (BAL || (a.score == MOE_SCORE_SOFTMAX && (BIAS || !a.renorm))) {
+          z = 0.0f;
+          float ex[NREG];
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) { ex[i] = exp_f(l[i] - m); z += ex[i]; }
+          z = wave_sum(z);
+          if constexpr (BAL) {
+            ++tv;
+            const float lse = m + LN2 * __builtin_amdgcn_logf(z);
+            zsum += lse * lse;
+            if (a.score == MOE_SCORE_SOFTMAX) {
+              const float inv = 1.0f / z;
+#pragma unroll
+              for (int i = 0; i < NREG; ++i) psum[i] += ex[i] * inv;
+            } else {
+              float s = 0.0f;
+#pragma unroll
+              for (int i = 0; i < NREG; ++i) { ex[i] = sigmoid_over(l[i], __builtin_fminf(m, 0.0f)); s += ex[i]; }
+              const float inv = 1.0f / wave_sum(s);           // at least half of one term
+#pragma unroll
+              for (int i = 0; i < NREG; ++i) psum[i] += ex[i] * inv;
+            }
+          }
+        }
+        float logit;
+        choose<VEC, NREG, BIAS>(l, a.bias, a.E, a.K, a.score, m, z, cand, lane, id, logit);
+        // with renorm relative to the largest chosen logit: the sum is at least half of that one's term
+        float top = a.score == MOE_SCORE_SOFTMAX ? m : 0.0f;
+        if (a.renorm) top = __builtin_fminf(wave_max(logit), top);
+        const float s = id < 0 ? 0.0f : a.score == MOE_SCORE_SOFTMAX ? exp_f(logit - top) : sigmoid_over(logit, top);
+        const float den = a.renorm ? wave_sum(s) : a.score == MOE_SCORE_SOFTMAX ? z : 1.0f;
+        w = id < 0 ? 0.0f : a.scale * (s / den);
+        if constexpr (BAL)
+          if (id >= 0) atomicAdd(&hist[id], 1);
+      }
+    }
+    if (lane < a.K) {
+      a.ids[t * a.K + lane] = id;
+      a.w[t * a.K + lane] = w;
+    }
+  }
+  if constexpr (BAL) {
+    const BalanceParts b = balance_parts(ws, a.E);
+    int* const small = reinterpret_cast<int*>(handed);        // tv and z of each wave first
+    __syncthreads();
+    if (lane == 0) { small[2 * wave] = tv; small[2 * wave + 1] = __float_as_int(zsum); }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int n = 0;
+      float q = 0.0f;
+      for (int i = 0; i < waves; ++i) { n += small[2 * i]; q += __int_as_float(small[2 * i + 1]); }
+      b.tv[blockIdx.x] = n;
+      b.z[blockIdx.x] = q;
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) b.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
+    // the waves' sums: at most HAND waves at a time hand theirs to as many lower ones, until one is left
+    for (int left = waves; left > 1;) {
+      const int n = left / 2 < HAND ? left / 2 : HAND;        // waves [left - n, left) hand to [left - 2 n, left - n)
+      __syncthreads();
+      if (wave >= left - n && wave < left) {
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) {
+          const int col = column<VEC>(i, lane);
+          if (col < a.E) handed[(wave - left + n) * a.E + col] = psum[i];
+        }
+      }
+      __syncthreads();
+      if (wave >= left - 2 * n && wave < left - n) {
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) {
+          const int col = column<VEC>(i, lane);
+          if (col < a.E) psum[i] += handed[(wave - left + 2 * n) * a.E + col];
+        }
+      }
+      left -= n;
+    }
+    if (wave == 0) {
+#pragma unroll
+      for (int i = 0; i < NREG; ++i) {
+        const int col = column<VEC>(i, lane);
+        if (col < a.E) b.psum[(int64_t)blockIdx.x * a.E + col] = psum[i];
+      }
+    }
+  }
+}
+
+// The batch's statistics from the workgroups' partial sums, 64 experts per workgroup: 16 row
+// classes add their partial rows in order, then the classes are added in order.  The workgroup
+// that takes the last ticket adds the workgroups' loss parts, again in order.
+__global__ __launch_bounds__(1024) void balance_finish_kernel(const RouterArgs a, const BalanceArgs o, void* ws, int parts) {
+  __shared__ float ps[16][64];
+  __shared__ int cs[16][64];
+  __shared__ int s_tv;
+  __shared__ float s_z;
+  const BalanceParts b = balance_parts(ws, a.E);
+  const int lane = threadIdx.x & 63, rc = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
+  float p = 0.0f;
+  int c = 0;
+  if (e < a.E)
+    for (int i = rc; i < parts; i += 16) {
+      p += b.psum[(int64_t)i * a.E + e];
+      c += b.counts[(int64_t)i * a.E + e];
+    }
+  ps[rc][lane] = p;
+  cs[rc][lane] = c;
+  if (rc == 0) {
+    int n = 0;
+    float q = 0.0f;
+    for (int i = lane; i < parts; i += 64) { n += b.tv[i]; q += b.z[i]; }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, WAVE);
+    q = wave_sum(q);
+    if (lane == 0) { s_tv = n; s_z = q; }
+  }
+  __syncthreads();
+  if (rc != 0) return;
+  for (int i = 1; i < 16; ++i) { p += ps[i][lane]; c += cs[i][lane]; }
+  const int tv = s_tv;
+  const float mean = tv > 0 ? p / (float)tv : 0.0f;
+  float part = 0.0f;
+  if (e < a.E) {
+    o.counts[e] = c;
+    o.mean_prob[e] = mean;
+    part = (float)c * mean;
+  }
+  part = wave_sum(part);
+  if (lane != 0) return;
+  float total = part;
+  if (gridDim.x > 1) {
+    __hip_atomic_store(&b.loss[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int ticket = __hip_atomic_fetch_add(b.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (ticket != (int)gridDim.x - 1) return;
+    total = 0.0f;
+    for (unsigned i = 0; i < gridDim.x; ++i)
+      total += __hip_atomic_load(&b.loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  o.num_valid[0] = tv;
+  o.loss[0] = tv > 0 ? o.coef * total * ((float)a.E / ((float)a.K * (float)tv)) : 0.0f;
+  o.loss[1] = tv > 0 && o.z_coef != 0.0f ? o.z_coef * s_z / (float)tv : 0.0f;   // s_z may be infinite
+}
+
+// d_logits of one row per wave.  With t_k the gradient that reaches the chosen expert k through
+// its weight (times ds/dl), a_i = d_loss[0] coef c_i E / (K Tv^2):
+//   softmax: dl_i = t_i - p_i sum t + p_i (a_i - sum a p);  sigmoid: t_i + p_i (1 - s_i) (a_i - sum a p)
+// plus d_loss[1] z_coef 2 lse / Tv softmax(l)_i.  t is spread over the row through LDS; an expert
+// that the ids name twice gets the sum.
+template <class LT, int VEC, int NREG>
+__global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a, const BalanceArgs o,
+                                                              const float* __restrict__ dw,
+                                                              const float* __restrict__ dloss,
+                                                              LT* __restrict__ dlogits) {
+  extern __shared__ float spread[];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  float* const t_row = spread + wave * a.E;
+  for (int e = lane; e < a.E; e += 64) t_row[e] = 0.0f;
+  wave_sync();
+  const int tv = o.counts ? *o.num_valid : 0;
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX;
+  const float db = o.counts && tv > 0 ? (dloss ? dloss[0] : 1.0f) * o.coef : 0.0f;
+  const float dz = o.counts && tv > 0 ? (dloss ? dloss[1] : 1.0f) * o.z_coef * 2.0f / (float)tv : 0.0f;
+  float f[NREG];
+  {
+    const float k = tv > 0 ? db * (float)a.E / ((float)a.K * (float)tv * (float)tv) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) {
+      const int col = column<VEC>(i, lane);
+      f[i] = o.counts && col < a.E ? k * (float)o.counts[col] : 0.0f;
+    }
+  }
+  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves) {
+    const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
+    LT* const out = dlogits + t * a.E;
+    float l[NREG];
+    float m = -INFINITY;
+    if (!a.valid || a.valid[t]) {
+      load_logits<LT, VEC, NREG>(row, a.E, lane, l);
+#pragma unroll
+      for (int i = 0; i < NREG; ++i) m = __builtin_fmaxf(m, l[i]);
+      m = wave_max(m);
+    }
+    if (!(m > -INFINITY)) {                                   // a row that chose nothing
+#pragma unroll
+      for (int i = 0; i < NREG; ++i) l[i] = 0.0f;
+    } else {
+      float z = 1.0f, inv_z = 1.0f;
+      const bool need_p = (softmax && (o.counts || !a.renorm)) || dz != 0.0f;
+      if (need_p) {
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) z += exp_f(l[i] - m);
+        z = wave_sum(z);
+        inv_z = 1.0f / z;
+      }
+      // the chosen experts' part
+      float tsum = 0.0f;
+      int id = -1;
+      if (dw) {
+        float v = 0.0f, g = 0.0f, lk = -INFINITY;
+        if (lane < a.K) {
+          id = a.ids[t * a.K + lane];
+          if ((unsigned)id >= (unsigned)a.E) id = -1;
+        }
+        if (id >= 0) {
+          float one[1];
+          load_row<1>(row + id, one);
+          lk = one[0] > -INFINITY ? __builtin_fminf(one[0], BIG) : -INFINITY;
+          g = a.scale * dw[t * a.K + lane];
+          v = softmax ? exp_f(lk - m) * inv_z : fast_sigmoid(lk);
+        }
+        float tk;
+        if (a.renorm) {
+          const float top = __builtin_fminf(wave_max(lk), softmax ? m : 0.0f);
+          const bool on = lk > -INFINITY;
+          const float e = !on ? 0.0f : softmax ? exp_f(lk - top) : sigmoid_over(lk, top);
+          const float total = wave_sum(e);
+          const float w = on ? e / total : 0.0f;
+          const float mean = wave_sum(w * g);
+          tk = w * (g - mean);                                // softmax: sums to 0 over the chosen
+        } else {
+          tk = v * g;
+          tsum = softmax ? wave_sum(tk) : 0.0f;
+        }
+        if (!softmax) tk *= 1.0f - v;
+        if (id >= 0) atomicAdd(&t_row[id], tk);
+        wave_sync();
+      }
+      const float lse = m + LN2 * __builtin_amdgcn_logf(z);
+      const float kz = dz != 0.0f ? dz * lse * inv_z : 0.0f;
+      if (softmax) {
+        float mean = 0.0f;
+        if (o.counts) {
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) mean += f[i] * exp_f(l[i] - m);
+          mean = wave_sum(mean) * inv_z;
+        }
+        const float base = mean + tsum;
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) {
+          const int col = column<VEC>(i, lane);
+          const float ex = need_p ? exp_f(l[i] - m) : 0.0f;
+          l[i] = ex * (inv_z * (f[i] - base) + kz) + (dw && col < a.E ? t_row[col] : 0.0f);
+        }
+      } else {
+        const float top = __builtin_fminf(m, 0.0f);
+        float s = 1.0f, mean = 0.0f;
+        if (o.counts) {
+          s = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) {
+            const float si = sigmoid_over(l[i], top);
+            s += si;
+            mean += f[i] * si;
+          }
+          s = wave_sum(s);
+          mean = wave_sum(mean);
+        }
+        const float inv_s = 1.0f / s;                         // at least half of one term
+        mean *= inv_s;
+#pragma unroll
+        for (int i = 0; i < NREG; ++i) {
+          const int col = column<VEC>(i, lane);
+          float d = dw && col < a.E ? t_row[col] : 0.0f;
+          if (o.counts) d += sigmoid_over(l[i], top) * (1.0f - fast_sigmoid(l[i])) * (f[i] - mean) * inv_s;
+          if (kz != 0.0f) d += kz * exp_f(l[i] - m);
+          l[i] = d;
+        }
+      }
+      if (dw) {
+        wave_sync();
+        if (id >= 0) t_row[id] = 0.0f;
+        wave_sync();
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < NREG / VEC; ++c) {
+      const int col = (c * 64 + lane) * VEC;
+      if (col < a.E) {
+        float v[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] = l[c * VEC + j];
+        store_row<VEC>(out + col, v);
+      }
+    }
+  }
+}
+
+// 8 consecutive logits per lane (16-byte accesses) for rows that allow it and fill most lanes;
+// one per lane otherwise (rows of up to 256 experts leave too few lanes a maximum to bound the
+// choice with, and are short anyway).
+bool wide_rows(int E, const void* p, const void* q) {
+  return E > 256 && E % 8 == 0 && !(((uintptr_t)p | (uintptr_t)q) & 15);
+}
+
+template <class LT, int VEC, int NREG>
+void forward_rows(const RouterArgs& a, bool bal, int parts, void* ws, hipStream_t s) {
+  if (bal) {
+    constexpr int waves = MOE_ROUTER_WAVES;
+    const size_t lds = waves * CAND * sizeof(uint2) + (size_t)(1 + HAND) * a.E * 4 + 256;
+    if (a.bias) router_kernel<LT, VEC, NREG, true, true><<<parts, waves * 64, lds, s>>>(a, ws);
+    else router_kernel<LT, VEC, NREG, false, true><<<parts, waves * 64, lds, s>>>(a, ws);
+  } else {
+    constexpr int waves = 4;
+    const unsigned grid = (unsigned)((a.T + waves - 1) / waves);
+    if (a.bias) router_kernel<LT, VEC, NREG, true, false><<<grid, waves * 64, waves * CAND * sizeof(uint2), s>>>(a, nullptr);
+    else router_kernel<LT, VEC, NREG, false, false><<<grid, waves * 64, waves * CAND * sizeof(uint2), s>>>(a, nullptr);
+  }
+}
+
+template <class LT>
+void forward(const RouterArgs& a, bool bal, int parts, void* ws, hipStream_t s) {
+  if (wide_rows(a.E, a.logits, nullptr)) {
+    if (a.E <= 512) forward_rows<LT, 8, 8>(a, bal, parts, ws, s);
+    else if (a.E <= 1024) forward_rows<LT, 8, 16>(a, bal, parts, ws, s);
+    else forward_rows<LT, 8, 32>(a, bal, parts, ws, s);
+  } else {
+    if (a.E <= 256) forward_rows<LT, 1, 4>(a, bal, parts, ws, s);
+    else if (a.E <= 1024) forward_rows<LT, 1, 16>(a, bal, parts, ws, s);
+    else forward_rows<LT, 1, 32>(a, bal, parts, ws, s);
+  }
+}
+
+template <class LT>
+void backward(const RouterArgs& a, const BalanceArgs& o, const float* dw, const float* dloss, void* dlogits, hipStream_t s) {
+  const unsigned groups = (unsigned)((a.T + 3) / 4);
+  const unsigned grid = groups < 1024u ? groups : 1024u;
+  const size_t lds = (size_t)4 * a.E * 4;
+  LT* const d = static_cast<LT*>(dlogits);
+  if (wide_rows(a.E, a.logits, dlogits)) {
+    if (a.E <= 512) router_backward_kernel<LT, 8, 8><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+    else if (a.E <= 1024) router_backward_kernel<LT, 8, 16><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+    else router_backward_kernel<LT, 8, 32><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+  } else {
+    if (a.E <= 256) router_backward_kernel<LT, 1, 4><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+    else if (a.E <= 1024) router_backward_kernel<LT, 1, 16><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+    else router_backward_kernel<LT, 1, 32><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_router(const RouterArgs& a, const BalanceArgs* b, void* ws, hipStream_t s) {
+  const int groups = (a.T + MOE_ROUTER_WAVES - 1) / MOE_ROUTER_WAVES;
+  const int parts = groups < 1 ? 1 : groups < MOE_ROUTER_PARTS ? groups : MOE_ROUTER_PARTS;
+  if (a.dt == MOE_DT_F32) forward<float>(a, b != nullptr, parts, ws, s);
+  else forward<uint16_t>(a, b != nullptr, parts, ws, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !b) return e;
+  balance_finish_kernel<<<(unsigned)((a.E + 63) / 64), 1024, 0, s>>>(a, *b, ws, parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_backward(const RouterArgs& a, const BalanceArgs* b, const float* dw, const float* dloss,
+                                  void* dlogits, hipStream_t s) {
+  BalanceArgs none = {};
+  if (a.dt == MOE_DT_F32) backward<float>(a, b ? *b : none, dw, dloss, dlogits, s);
+  else backward<uint16_t>(a, b ? *b : none, dw, dloss, dlogits, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe
