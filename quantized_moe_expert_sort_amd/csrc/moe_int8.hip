@@ -115,156 +115,160 @@ __device__ __forceinline__ void store_one(const Gemm& p, int64_t t, int c, float
 // ---------------------------------------------------------------- few tokens: weights streamed
 //
 // A workgroup takes one 16-channel block (with an activation the gate block and the up block of
-// the same outputs) and up to 16 * MT tokens; its waves split K and add their sums through LDS.
-// The weights are read once, from packed blocks of whole lines, straight into the operand
-// registers.  Bound by the weights' bytes.
+// the same outputs) and 16 tokens; its waves split K and add their sums through LDS.  The weights
+// are read once, from packed blocks of whole lines, straight into the operand registers, up to
+// seven blocks (and as many of the gate) in flight per wave before the first MFMA.  Bound by the
+// weights' bytes: 7168 x 3584 at 1 token 7.5 us, 3584 x 3584 5.5 us, so 3.6 us that do not depend
+// on the bytes and 6.7 TB/s beyond (four blocks in flight and 16 waves: 7.8 and 5.7 us).
 
-template <int MT, bool ACT>
-__global__ __launch_bounds__(1024) void gemm_i8_stream_kernel(const Gemm p, int blocks_k) {
+constexpr int STREAM_U = 7;                   // K blocks a wave loads together
+constexpr int STREAM_WAVES = 8;               // waves of a workgroup, at most
+
+template <bool ACT>
+__global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_i8_stream_kernel(const Gemm p, int blocks_k) {
   constexpr int NB = ACT ? 2 : 1;
-  extern __shared__ __align__(16) uint8_t lds[];
-  v4i* const sums = reinterpret_cast<v4i*>(lds);              // [waves][NB * MT][64]
+  __shared__ v4i sums[STREAM_WAVES][NB][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
-  const int t0 = blockIdx.y * 16 * MT;
   const uint8_t* wp[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
     wp[b] = p.w + ((int64_t)blockIdx.x + (b ? p.No / 16 : 0)) * blocks_k * 1024 + lane * 16;
-  const uint8_t* ap[MT];
+  const uint8_t* const ap = p.a + (int64_t)min(r, p.T - 1) * p.K;
+  v4i acc[NB];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) ap[m] = p.a + (int64_t)min(t0 + 16 * m + r, p.T - 1) * p.K;
-  v4i acc[NB][MT];
+  for (int b = 0; b < NB; ++b) acc[b] = v4i{0, 0, 0, 0};
+  const int steps = (p.K + 63) / 64;                          // the padding past them is not read
+  const int per = (steps + waves - 1) / waves;
+  const int s1 = min((wave + 1) * per, steps);
+  for (int s0 = wave * per; s0 < s1; s0 += STREAM_U) {
+    uint4 wv[STREAM_U][NB], av[STREAM_U];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+    for (int j = 0; j < STREAM_U; ++j) {
+      const int s = min(s0 + j, s1 - 1);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[b][m] = v4i{0, 0, 0, 0};
-  const int per = (blocks_k + waves - 1) / waves;
-  const int s1 = min((wave + 1) * per, blocks_k);
-#pragma unroll 4
-  for (int s = wave * per; s < s1; ++s) {
-    uint4 wv[NB], av[MT];
+      for (int b = 0; b < NB; ++b) wv[j][b] = ldw16(wp[b] + (int64_t)s * 1024);
+      av[j] = *reinterpret_cast<const uint4*>(ap + min(s * 64 + g * 16, p.K - 16));   // past K the weights are zero
+    }
 #pragma unroll
-    for (int b = 0; b < NB; ++b) wv[b] = ldw16(wp[b] + (int64_t)s * 1024);
-    const int k = min(s * 64 + g * 16, p.K - 16);             // past K the weights are zero
+    for (int j = 0; j < STREAM_U; ++j)
+      if (s0 + j < s1) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) av[m] = *reinterpret_cast<const uint4*>(ap[m] + k);
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        acc[b][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wv[b]), __builtin_bit_cast(v4i, av[m]),
-                                                          acc[b][m], 0, 0, 0);
+        for (int b = 0; b < NB; ++b)
+          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wv[j][b]), __builtin_bit_cast(v4i, av[j]),
+                                                         acc[b], 0, 0, 0);
+      }
   }
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) sums[(wave * NB * MT + b * MT + m) * 64 + lane] = acc[b][m];
+  for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b];
   __syncthreads();
-  // wave m finishes token tile m: lane (g, r) has channels 4 g .. 4 g + 3 of token r
-  for (int m = wave; m < MT; m += waves) {
-    v4i tot[NB];
+  if (wave != 0 || r >= p.T) return;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      tot[b] = v4i{0, 0, 0, 0};
-      for (int w = 0; w < waves; ++w) tot[b] += sums[(w * NB * MT + b * MT + m) * 64 + lane];
-    }
-    const int64_t t = t0 + 16 * m + r;
-    if (t < p.T) {
-      const float sa = p.sa[t];
-      const int c0 = blockIdx.x * 16 + 4 * g;
+  for (int b = 0; b < NB; ++b)
+    for (int w = 1; w < waves; ++w) acc[b] += sums[w][b][lane];
+  const float sa = p.sa[r];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + i;
-        if (c < p.No) {
-          float v = (float)tot[0][i] * (sa * p.sw[c]);
-          if constexpr (ACT) v = activate(p, v, (float)tot[1][i] * (sa * p.sw[p.No + c]));
-          store_one(p, t, c, v);
-        }
-      }
+  for (int i = 0; i < 4; ++i) {                               // channels 4 g .. 4 g + 3 of token r
+    const int c = blockIdx.x * 16 + 4 * g + i;
+    if (c < p.No) {
+      float v = (float)acc[0][i] * (sa * p.sw[c]);
+      if constexpr (ACT) v = activate(p, v, (float)acc[1][i] * (sa * p.sw[p.No + c]));
+      store_one(p, r, c, v);
     }
   }
 }
 
-// ---------------------------------------------------------------- many tokens: LDS tiles
+// ---------------------------------------------------------------- more tokens: LDS tiles
 //
-// Tiles of BM tokens x BN weight rows, K in steps of 128 bytes through two LDS buffers filled by
-// the load-to-LDS copies.  Four waves in a 2 x 2 grid, each BM/2 x BN/2 with 32x32x32 MFMAs; LDS
-// holds the operands as the same 1 KB blocks of 16 rows x 64 bytes in lane order, so a copy
-// instruction fills a block and an operand read is two runs of 256 consecutive bytes per half wave.
-// The operands of the next quarter step are read while the matrix cores work on the present one,
-// also across the barrier between two steps.
+// Tiles of BM tokens x BN weight rows, K in steps of 128 bytes through S LDS buffers filled by the
+// load-to-LDS copies (S - 1 steps in flight).  GM x GN waves, each BM/GM tokens x BN/GN weight rows
+// with 32x32x32 MFMAs; with KG > 1 that many groups of waves share out K and add their sums through
+// LDS.  The operands of the next quarter step are read while the matrix cores work on the present
+// one, also across the barrier between two steps.
+//
+// A copy instruction takes 8 token rows x 128 bytes (whole lines: 16 rows x 64 bytes ran at half
+// the rate), its 16-byte pieces placed at p ^ ((row / 2) % 8) so that the 16 lanes that read one
+// piece of 16 rows hit distinct banks, or one 1 KB weight block, which stays in lane order.  LDS
+// bank conflicts: none counted.
+//
+// Measured (cold weights and tokens, K 3584): one round of tiles on 256 CUs takes 8.1 us at 32 x 64
+// (KG 4), 10.2 at 64 x 64 (KG 2), 11.6 at 64 x 64, 18 at 128 x 128, 28 at 128 x 256 and 48 at
+// 256 x 256: the smaller the tile, the more it is bound by the copies, which run at 45 to 50 bytes
+// a nanosecond and CU (140 from a warm L2).  At 8192^3 the 256 x 256 tiles reach 2410 TOP/s (the
+// matrix cores busy 61% of the time at 1.74 GHz, the clock the power limit leaves); without the
+// copies the same loop runs 1.5 times as fast, without the MFMAs 1.2 times.
 
 __device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 
-template <int BM, int BN, bool ACT>
-__global__ __launch_bounds__(256) void gemm_i8_tile_kernel(const Gemm p, int blocks_k, int tiles_m, int tiles_n) {
-  constexpr int WM = BM / 2, WN = BN / 2;                     // one wave's tokens and weight rows
-  constexpr int FM = WM / 32, FN = WN / 32;                   // its 32-row operands
-  constexpr int A_BYTES = BM * 128, BUF = (BM + BN) * 128;
-  constexpr int QA = BM / 16 * 2 / 4, QB = BN / 16 * 2 / 4;   // copy instructions of a wave and step
-  static_assert(!ACT || FN % 2 == 0, "gate and up operands in pairs");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * BUF];
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
+template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
+struct Tile {
+  static constexpr int WAVES = GM * GN, THREADS = WAVES * KG * 64;
+  static constexpr int BUF = (BM + BN) * 128, LDS = KG * S * BUF;
+};
 
-  // Workgroup b runs on XCD b % 8.  Each XCD takes a run of consecutive tiles, in columns of GM
-  // tiles down the tokens, so that the tiles it works on at one time share rows in its L2.
-  constexpr int GM = 4;
-  const int tiles = tiles_m * tiles_n;
-  int id;
-  {
-    const int x = blockIdx.x & 7, i = blockIdx.x >> 3, q = tiles >> 3, rem = tiles & 7;
-    id = x * q + min(x, rem) + i;
-  }
-  const int per_group = GM * tiles_n, grp = id / per_group, in = id - grp * per_group;
-  const int gm = min(GM, tiles_m - grp * GM);
-  const int tm = grp * GM + in % gm, tn = in / gm;
+template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
+__device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, int tn, uint8_t* lds_all) {
+  using T = Tile<BM, BN, GM, GN, S, KG, ACT>;
+  constexpr int WAVES = T::WAVES, BUF = T::BUF;
+  constexpr int WM = BM / GM, WN = BN / GN;                   // one wave's tokens and weight rows
+  constexpr int FM = WM / 32, FN = WN / 32;                   // its 32-row operands
+  constexpr int A_BYTES = BM * 128;
+  constexpr int QA = BM / 8 / WAVES, QB = BN / 8 / WAVES;     // copy instructions of a wave and step
+  constexpr int Q = QA + QB;
+  static_assert(!ACT || FN % 2 == 0, "gate and up operands in pairs");
+  static_assert(QA * 8 * WAVES == BM && QB * 8 * WAVES == BN && (S - 2) * Q < 63 && S >= 2 && S <= 4, "whole copies");
+  static_assert(KG == 1 || (KG - 1) * WAVES * FN * FM * 4096 <= T::LDS, "the groups' sums fit");
+  const int all = blocks_k / 2, most = (all + KG - 1) / KG;   // every step starts inside K
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG == 1 ? 0 : wave_all / WAVES, wave = KG == 1 ? wave_all : wave_all % WAVES;
+  const int first = kg * most, steps = max(min(most, all - first), 0);   // this group's steps
+  uint8_t* const lds = lds_all + kg * (S * BUF);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+  const int wm = wave % GM, wn = wave / GM;
   const int t0 = tm * BM;
   const int c0 = ACT ? tn * (BN / 2) : tn * BN;               // first output channel
-  const int last_f = (p.N + 15) / 16 - 1;
 
   // per-lane source offsets of this wave's copies
-  const int r = lane & 15, g = lane >> 4;
-  const uint8_t* a_base = p.a + (int64_t)t0 * p.K;
+  const uint8_t* const a_base = p.a + (int64_t)t0 * p.K;
   uint32_t a_off[QA], b_off[QB];
+  int a_piece[QA];
 #pragma unroll
   for (int q = 0; q < QA; ++q) {
-    const int blk = wave + 4 * q;                             // (16-row group, half step)
-    a_off[q] = (uint32_t)min((blk >> 1) * 16 + r, p.T - 1 - t0) * (uint32_t)p.K + (blk & 1) * 64 + g * 16;
+    const int row = (wave + WAVES * q) * 8 + (lane >> 3);
+    a_piece[q] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    a_off[q] = (uint32_t)min(row, p.T - 1 - t0) * (uint32_t)p.K + a_piece[q];
   }
 #pragma unroll
   for (int q = 0; q < QB; ++q) {
-    const int blk = wave + 4 * q, rg = blk >> 1;              // 16-row group of the tile
+    const int blk = wave + WAVES * q, rg = blk >> 1;          // 16-row group of the tile, half step
     int f;
     if (ACT) {                                                // each wave's rows: its gate rows, then the up rows
       const int w = rg / (WN / 16), i = rg % (WN / 16), half = WN / 32;
       const int gf = min(c0 / 16 + w * half + i % half, p.No / 16 - 1);
       f = i < half ? gf : p.No / 16 + gf;
     } else {
-      f = min(c0 / 16 + rg, last_f);
+      f = min(c0 / 16 + rg, (p.N + 15) / 16 - 1);
     }
     b_off[q] = (uint32_t)f * (uint32_t)blocks_k * 1024u + (blk & 1) * 1024 + lane * 16;
   }
-  const int steps = blocks_k / 2;
-  const auto fetch = [&](int ks) {
-    const uint32_t buf = lds0 + (ks & 1) * BUF;
-    const uint8_t* ab = a_base + ks * 128;
-    const uint8_t* bb = p.w + (int64_t)ks * 2048;
-    const bool tail = ks * 128 + 128 > p.K;
+  int fill = 0;                                               // the buffer that the next step's copies fill
+  const auto fetch = [&](int st) {
+    const uint32_t buf = lds0 + fill * BUF;
+    fill = fill + 1 == S ? 0 : fill + 1;
+    st += first;
+    const int left = p.K - st * 128;                          // bytes of a row from this step on, >= 16
+    const uint8_t* ab = a_base + st * 128;
+    const uint8_t* bb = p.w + (int64_t)st * 2048;
 #pragma unroll
     for (int q = 0; q < QA; ++q) {
-      const int blk = wave + 4 * q;
       uint32_t off = a_off[q];
-      // past K the weights are zero: read the row's last 16 bytes instead
-      if (tail) off -= max((blk & 1) * 64 + g * 16 + 16 - (p.K - ks * 128), 0);
-      copy16(ab, off, buf + blk * 1024);
+      if (left < 128) off -= max(a_piece[q] + 16 - left, 0);  // past K the weights are zero: any bytes of the row
+      copy16(ab, off, buf + (wave + WAVES * q) * 1024);
     }
 #pragma unroll
-    for (int q = 0; q < QB; ++q) copy16(bb, b_off[q], buf + A_BYTES + (wave + 4 * q) * 1024);
+    for (int q = 0; q < QB; ++q) copy16(bb, b_off[q], buf + A_BYTES + (wave + WAVES * q) * 1024);
   };
 
   v16i acc[FN][FM];
@@ -275,17 +279,19 @@ __global__ __launch_bounds__(256) void gemm_i8_tile_kernel(const Gemm p, int blo
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[n][m][i] = 0;
 
-  // operand (16-row groups 2 k, 2 k + 1), quarter step ss: lane l holds row l % 32
-  const int frag = ((lane >> 4) & 1) * 2048 + ((lane >> 5) * 16 + r) * 16;
-  const uint8_t* const fa = lds + wm * (WM / 16) * 2048 + frag;
-  const uint8_t* const fb = lds + A_BYTES + wn * (WN / 16) * 2048 + frag;
+  // 32-row operands, quarter step ss: lane l holds bytes 32 ss + 16 (l / 32) .. + 15 of row l % 32
+  const int l32 = lane & 31, hl = lane >> 5;
+  const uint8_t* const fa = lds + (wm * WM + l32) * 128;
+  const int a_swz = (l32 >> 1) & 7;                           // a wave's rows start at a multiple of 32
+  const uint8_t* const fb = lds + A_BYTES + wn * (WN / 16) * 2048 + (l32 >> 4) * 2048 + (hl * 16 + (lane & 15)) * 16;
   v4i av[2][FM], bv[2][FN];
-  const auto read = [&](int set, int ks, int ss) {
-    const int at = (ks & 1) * BUF + (ss >> 1) * 1024 + (ss & 1) * 512;
+  const auto read = [&](int set, int buf, int ss) {
 #pragma unroll
-    for (int n = 0; n < FN; ++n) bv[set][n] = *reinterpret_cast<const v4i*>(fb + at + n * 4096);
+    for (int n = 0; n < FN; ++n)
+      bv[set][n] = *reinterpret_cast<const v4i*>(fb + buf * BUF + (ss >> 1) * 1024 + (ss & 1) * 512 + n * 4096);
 #pragma unroll
-    for (int m = 0; m < FM; ++m) av[set][m] = *reinterpret_cast<const v4i*>(fa + at + m * 4096);
+    for (int m = 0; m < FM; ++m)
+      av[set][m] = *reinterpret_cast<const v4i*>(fa + buf * BUF + (((2 * ss + hl) ^ a_swz) * 16) + m * 4096);
   };
   const auto mul = [&](int set) {
 #pragma unroll
@@ -294,31 +300,63 @@ __global__ __launch_bounds__(256) void gemm_i8_tile_kernel(const Gemm p, int blo
       for (int m = 0; m < FM; ++m)
         acc[n][m] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bv[set][n], av[set][m], acc[n][m], 0, 0, 0);
   };
-  // every copy of this wave has landed and its LDS reads are done; then meet the other waves
-  const auto meet = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  // All but the newest `later` steps' copies of this wave have landed and its LDS reads are done;
+  // then meet the other waves.
+  const auto meet = [&](int later) {
+    if (later >= S - 2) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * Q) : "memory");
+    else if (S > 3 && later == 1) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(Q) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  };
 
-  fetch(0);
-  meet();
-  if (steps > 1) fetch(1);
-  read(0, 0, 0);
-  for (int ks = 0; ks < steps; ++ks) {
-    read(1, ks, 1);
-    mul(0);
-    read(0, ks, 2);
-    mul(1);
-    read(1, ks, 3);
-    mul(0);
-    if (ks + 1 < steps) {
-      meet();                                                 // buffer ks + 1 is filled, buffer ks is free
-      if (ks + 2 < steps) fetch(ks + 2);
-      read(0, ks + 1, 0);
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i)
+    if (i < steps) fetch(i);
+  meet(min(steps - 1, S - 2));
+  int buf = 0;
+  if (KG == 1 || steps > 0) read(0, 0, 0);
+  for (int st = 0; st < most; ++st) {                         // as many steps, so barriers, for every group
+    // the buffer of step st - 1 is free: every wave has passed the barrier after reading it
+    if (st + S - 1 < steps) fetch(st + S - 1);
+    const bool work = KG == 1 || st < steps;
+    if (work) {
+#pragma unroll
+      for (int ss = 0; ss < 3; ++ss) {
+        read((ss + 1) & 1, buf, ss + 1);
+        mul(ss & 1);
+      }
     }
-    mul(1);
+    buf = buf + 1 == S ? 0 : buf + 1;
+    if (st + 1 < most) {
+      meet(min(steps - 2 - st, S - 2));
+      if (KG == 1 || st + 1 < steps) read(0, buf, 0);
+    }
+    if (work) mul(1);
+  }
+  if constexpr (KG > 1) {                                     // the groups' sums, added by the first group
+    v4i* const part = reinterpret_cast<v4i*>(lds_all);
+    constexpr int V = FN * FM * 4;
+    __syncthreads();                                          // every operand read is done
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const v16i& x = acc[i / 4 / FM][i / 4 % FM];
+        part[(((kg - 1) * WAVES + wave) * V + i) * 64 + lane] = v4i{x[i % 4 * 4], x[i % 4 * 4 + 1], x[i % 4 * 4 + 2], x[i % 4 * 4 + 3]};
+      }
+    }
+    __syncthreads();
+    if (kg > 0) return;
+#pragma unroll
+    for (int k = 0; k < KG - 1; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const v4i y = part[((k * WAVES + wave) * V + i) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i / 4 / FM][i / 4 % FM][i % 4 * 4 + j] += y[j];
+      }
   }
 
   // epilogue: register i of lane l is weight row 8 (i / 4) + 4 (l / 32) + i % 4, token l % 32
   constexpr int FO = ACT ? FN / 2 : FN;                       // 32-channel groups of outputs
-  const int hl = lane >> 5;
   const bool wide = p.No % 8 == 0 && !(((uintptr_t)p.out | (uintptr_t)p.add) & 15);
 #pragma unroll
   for (int n = 0; n < FO; ++n) {
@@ -368,29 +406,87 @@ __global__ __launch_bounds__(256) void gemm_i8_tile_kernel(const Gemm p, int blo
   }
 }
 
-template <int MT, bool ACT>
-void stream(const Gemm& p, int blocks_k, hipStream_t s) {
-  const unsigned nb = (unsigned)((p.No + 15) / 16);
-  const int waves = blocks_k >= 32 ? 8 : blocks_k >= 8 ? 4 : 2;
-  const size_t lds = (size_t)waves * (ACT ? 2 : 1) * MT * 1024;
-  gemm_i8_stream_kernel<MT, ACT><<<dim3(nb, (unsigned)((p.T + 16 * MT - 1) / (16 * MT))), waves * 64, lds, s>>>(p, blocks_k);
+// Tile number `id` of tiles_m x tiles_n: in columns of four tiles down the tokens, so that
+// neighbouring numbers share rows.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
+  constexpr int ROWS = 4;
+  const int per_group = ROWS * tiles_n, grp = id / per_group, in = id - grp * per_group;
+  const int rows = min(ROWS, tiles_m - grp * ROWS);
+  tm = grp * ROWS + in % rows;
+  tn = in / rows;
+}
+// Workgroup b runs on XCD b % 8: gives each XCD a run of consecutive numbers out of n, so that the
+// tiles it works on at one time share rows in its L2.
+__device__ __forceinline__ int run_of_xcd(int b, int n) {
+  const int x = b & 7, q = n >> 3, rem = n & 7;
+  return x * q + min(x, rem) + (b >> 3);
 }
 
-template <int BM, int BN, bool ACT>
-void tile(const Gemm& p, int blocks_k, hipStream_t s) {
-  const int tm = (p.T + BM - 1) / BM, cols = ACT ? BN / 2 : BN, tn = (p.No + cols - 1) / cols;
-  gemm_i8_tile_kernel<BM, BN, ACT><<<(unsigned)(tm * tn), 256, 0, s>>>(p, blocks_k, tm, tn);
+template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
+__global__ __launch_bounds__(GM * GN * KG * 64) void gemm_i8_tile_kernel(const Gemm p, int blocks_k, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<BM, BN, GM, GN, S, KG, ACT>::LDS];
+  int tm, tn;
+  tile_of(run_of_xcd(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  tile_body<BM, BN, GM, GN, S, KG, ACT>(p, blocks_k, tm, tn, lds);
+}
+
+// 256 x 256 tiles; those past the first `full` are taken in two halves of 128 tokens each, so that
+// a last round that would leave half of the CUs idle takes half as long.
+template <bool ACT>
+__global__ __launch_bounds__(512) void gemm_i8_big_kernel(const Gemm p, int blocks_k, int tiles_m, int tiles_n, int full) {
+  using Half = Tile<128, 256, 2, 4, 3, 1, ACT>;
+  static_assert(Half::LDS >= Tile<256, 256, 2, 4, 2, 1, ACT>::LDS, "both shapes share the LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Half::LDS];
+  int tm, tn;
+  if ((int)blockIdx.x < full) {
+    tile_of(run_of_xcd(blockIdx.x, full), tiles_m, tiles_n, tm, tn);
+    tile_body<256, 256, 2, 4, 2, 1, ACT>(p, blocks_k, tm, tn, lds);
+  } else {
+    const int h = run_of_xcd(blockIdx.x - full, gridDim.x - full);
+    tile_of(full + (h >> 1), tiles_m, tiles_n, tm, tn);
+    tm = 2 * tm + (h & 1);
+    if (tm * 128 < p.T) tile_body<128, 256, 2, 4, 3, 1, ACT>(p, blocks_k, tm, tn, lds);
+  }
 }
 
 template <bool ACT>
+int64_t tiles(const Gemm& p, int bm, int bn) {
+  const int cols = ACT ? bn / 2 : bn;
+  return (int64_t)((p.T + bm - 1) / bm) * ((p.No + cols - 1) / cols);
+}
+
+template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
+void tile(const Gemm& p, int blocks_k, hipStream_t s) {
+  using T = Tile<BM, BN, GM, GN, S, KG, ACT>;
+  const int tm = (p.T + BM - 1) / BM;
+  const int64_t n = tiles<ACT>(p, BM, BN);
+  gemm_i8_tile_kernel<BM, BN, GM, GN, S, KG, ACT><<<(unsigned)n, T::THREADS, 0, s>>>(p, blocks_k, tm, (int)(n / tm));
+}
+
+// Up to 16 tokens the weights are streamed; beyond, the smallest tiles that one round of CUS
+// workgroups holds (they take K in more groups), then the largest of which there is more than a
+// round.  Measured, K 3584, us: 64 tokens x 7168 (gate, up): streamed 15.6, 32 x 64 10.3, 64 x 64 in two
+// groups 12.2.  256 x 3584: 32 x 64 14.8, 64 x 64 in two groups 10.4, in one 12.1, 128 x 128 18.  256 x
+// 7168: 64 x 64 in two groups 22.8, in one 15.6, 128 x 128 18.2.  384 x 7168: 28.3, 19.3 (128 x 128).  512 x
+// 7168: 30, 21, 29 (256 x 256 in halves).  1024 x 7168: 56, 40, 34.
+template <bool ACT>
 void run(const Gemm& p, int blocks_k, hipStream_t s) {
-  if (p.T <= 16) stream<1, ACT>(p, blocks_k, s);
-  else if (p.T <= 32) stream<2, ACT>(p, blocks_k, s);
-  else if (p.T <= 64) stream<4, ACT>(p, blocks_k, s);
-  else {
-    const int64_t big = (int64_t)((p.T + 255) / 256) * ((p.N + 255) / 256);
-    if (big >= 192) tile<256, 256, ACT>(p, blocks_k, s);
-    else tile<128, 128, ACT>(p, blocks_k, s);
+  constexpr int CUS = 256;
+  if (p.T <= 16) {
+    const int steps = (p.K + 63) / 64, waves = (steps + STREAM_U - 1) / STREAM_U;
+    gemm_i8_stream_kernel<ACT><<<(unsigned)((p.No + 15) / 16), (waves < STREAM_WAVES ? waves : STREAM_WAVES) * 64, 0, s>>>(p, blocks_k);
+  } else if (tiles<ACT>(p, 32, 64) <= CUS) {
+    tile<32, 64, 1, ACT ? 1 : 2, 3, 4, ACT>(p, blocks_k, s);  // with ACT a wave holds a gate and an up operand
+  } else if (tiles<ACT>(p, 64, 64) <= CUS) {
+    tile<64, 64, 2, ACT ? 1 : 2, 3, 2, ACT>(p, blocks_k, s);
+  } else if (2 * tiles<ACT>(p, 128, 128) <= CUS) {
+    tile<64, 64, 2, ACT ? 1 : 2, 4, 1, ACT>(p, blocks_k, s);
+  } else if (tiles<ACT>(p, 128, 128) <= CUS) {
+    tile<128, 128, 4, 2, 4, 1, ACT>(p, blocks_k, s);
+  } else {
+    const int64_t n = tiles<ACT>(p, 256, 256);
+    const int tm = (p.T + 255) / 256, rest = (int)(n % CUS), full = (int)(2 * rest <= CUS ? n - rest : n);
+    gemm_i8_big_kernel<ACT><<<(unsigned)(full + 2 * (n - full)), 512, 0, s>>>(p, blocks_k, tm, (int)(n / tm), full);
   }
 }
 

@@ -64,6 +64,25 @@ def test_large_tiles(T, N, K, act):
     check(T, N, K, act, add=act is None)
 
 
+# (tokens, channels) of every tile shape the sizes choose between: 32 x 64 and 64 x 64 with K in groups,
+# 64 x 64, 128 x 128, 256 x 256 in halves, in halves with a half past the tokens, and full ones
+# before halves
+SHAPES = [(40, 200), (100, 3000), (300, 4000), (700, 4000), (1200, 4100), (1100, 4096), (4300, 4100)]
+
+
+@pytest.mark.parametrize("K", [16, 80, 128, 272, 400])
+@pytest.mark.parametrize("T,N", SHAPES)
+def test_tile_shapes(T, N, K):
+    check(T, N, K, add=K == 272)
+
+
+@pytest.mark.parametrize("K", [16, 144, 528])
+@pytest.mark.parametrize("T,N", SHAPES)
+@pytest.mark.parametrize("act", ["situv2", "silu"])
+def test_tile_shapes_with_activations(act, T, N, K):
+    check(T, (N + 31) // 32 * 32, K, act, add=K == 144)
+
+
 def test_sums_at_the_limits_of_int32():
     # all codes -128: 128 * 128 * K is the largest sum, just below 2^31
     K = (1 << 17) - 16
@@ -91,7 +110,7 @@ def test_a_token_does_not_depend_on_its_batch():
     d = {k: None if v is None else v.cuda() for k, v in c.items()}
     p = qm.moe_pack_i8(d["w"])
     full = qm.moe_gemm_i8(d["a"], d["sa"], p, d["sw"])
-    for n in (1, 17, 64, 65, 130):
+    for n in (1, 16, 17, 64, 65, 130):
         assert torch.equal(qm.moe_gemm_i8(d["a"][:n].clone(), d["sa"][:n].clone(), p, d["sw"]), full[:n])
 
 
