@@ -375,14 +375,14 @@ def i8_packed_shape(out_features, in_features):
     return ((out_features + 15) // 16, (in_features + 127) // 128 * 2, 1024)
 
 
-def _need(t, name, dtype, shape, device):
-    """The tensor's address (None for None), after its checks."""
+def _need(t, name, dtype, shape, index):
+    """The tensor's address (None for None), after its checks; index: the device's."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: need a dense {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{'a dense' if t.is_contiguous() else 'a strided'} {t.dtype} of {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: need a dense {dtype} tensor of shape {tuple(shape)} on device {index}, got "
+                     f"{'a dense' if t.is_contiguous() else 'a strided'} {t.dtype} of {tuple(t.shape)} on {t.device}")
 
 
 def _pick(table, key, name):
@@ -391,25 +391,32 @@ def _pick(table, key, name):
     return table[key]
 
 
-def _call(fn, device, *args):
-    """The library call on torch's current stream of `device`, with that device current."""
+# torch's getters without their lazy-initialisation wrappers: a call's tensors are on the GPU already
+# (2.7 us less of a call's 12 us on the host)
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(fn, index, *args):
+    """The library call on torch's current stream of device `index`, with that device current."""
     f = getattr(_lib or lib(), fn)
-    if device.index == torch.cuda.current_device():
-        status = f(*args, torch.cuda.current_stream().cuda_stream)
+    if index == _current_device():
+        status = f(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            status = f(*args, torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(index):
+            status = f(*args, _raw_stream(index))
     if status:
         _check(fn, status)
 
 
 def _on_gpu(t, name):
+    """(device, its index) of a tensor that has to be on the GPU."""
     if not t.is_cuda:
         raise ValueError(f"{name}: need a tensor on the GPU, got one on {t.device}")
-    return t.device
+    return t.device, t.get_device()
 
 
-def _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, device):
+def _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, index):
     if x.dim() != 2 or x.dtype not in _ROW_TYPES:
         raise ValueError(f"x: need a bfloat16 or float32 tensor [tokens, dim], got {x.dtype} of {tuple(x.shape)}")
     T, D = x.shape
@@ -418,13 +425,13 @@ def _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, dev
         raise ValueError("gate and gate_kind go together")
     p = BlockNormParams(tokens=T, dim=D, x_dt=_ROW_TYPES[x.dtype], gate_kind=kind,
                         gate_act=_pick(GATE_ACTS, gate_act, "gate_act"), scale=scale, eps=eps)
-    p.x = _need(x, "x", x.dtype, (T, D), device)
-    p.y = _need(y, "y", torch.bfloat16, (T, D), device)
-    p.w_post = _need(w_post, "w_post", torch.float32, (D,), device)
-    p.w_pre = _need(w_pre, "w_pre", torch.float32, (D,), device)
+    p.x = _need(x, "x", x.dtype, (T, D), index)
+    p.y = _need(y, "y", torch.bfloat16, (T, D), index)
+    p.w_post = _need(w_post, "w_post", torch.float32, (D,), index)
+    p.w_pre = _need(w_pre, "w_pre", torch.float32, (D,), index)
     if kind:
         p.gate = _need(gate, "gate", torch.bfloat16 if kind == 3 else torch.float32,
-                       ((D,), (T,), (T, D))[kind - 1], device)
+                       ((D,), (T,), (T, D))[kind - 1], index)
     return p, T, D
 
 
@@ -436,32 +443,32 @@ def moe_block_norm(x, y=None, *, w_post=None, gate=None, gate_kind="none", gate_
     Returns BlockNorm(h, n, q, q_scale, rstd): h as x (None without y; pass h=x to update the stream in
     place), n bf16 (None without w_pre or with want_n=False), q and q_scale for q_dtype "fp8", "fp4" or
     "i8", rstd [2, T] with stats=True (the backward pass needs it)."""
-    device = _on_gpu(x, "x")
-    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, device)
+    device, index = _on_gpu(x, "x")
+    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, index)
     n = q = q_scale = rstd = None
     if h is not None:
-        p.h = _need(h, "h", x.dtype, (T, D), device)
+        p.h = _need(h, "h", x.dtype, (T, D), index)
     elif y is not None:
         h = torch.empty_like(x)
         p.h = h.data_ptr()
     if w_pre is not None and want_n:
-        n = torch.empty((T, D), dtype=torch.bfloat16, device=device)
+        n = torch.empty(T, D, dtype=torch.bfloat16, device=device)
         p.n = n.data_ptr()
     if q_dtype is not None:
         p.q_dt = _pick(Q_DTYPES, q_dtype, "q_dtype")
         if w_pre is None:
             raise ValueError("q_dtype: there is nothing to code without w_pre")
         if p.q_dt == DT_I8:
-            q = torch.empty((T, D), dtype=torch.int8, device=device)
-            q_scale = torch.empty((T,), dtype=torch.float32, device=device)
+            q = torch.empty(T, D, dtype=torch.int8, device=device)
+            q_scale = torch.empty(T, dtype=torch.float32, device=device)
         else:
-            q = torch.empty((T, D if p.q_dt == DT_FP8 else D // 2), dtype=torch.uint8, device=device)
-            q_scale = torch.empty((T, D // 32), dtype=torch.uint8, device=device)
+            q = torch.empty(T, D if p.q_dt == DT_FP8 else D // 2, dtype=torch.uint8, device=device)
+            q_scale = torch.empty(T, D // 32, dtype=torch.uint8, device=device)
         p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
     if stats:
-        rstd = torch.empty((2, T), dtype=torch.float32, device=device)
+        rstd = torch.empty(2, T, dtype=torch.float32, device=device)
         p.rstd = rstd.data_ptr()
-    _call("moe_block_norm", device, p)
+    _call("moe_block_norm", index, p)
     return BlockNorm(h, n, q, q_scale, rstd)
 
 
@@ -470,12 +477,12 @@ def moe_block_norm_backward(x, y, rstd, dh, dn, *, w_post=None, gate=None, gate_
     """Gradients of moe_block_norm for its inputs, from those of h (dh, as x) and n (dn, bf16); either
     may be None.  rstd: as moe_block_norm(stats=True) returned it; the other arguments as given there.
     Returns BlockNormGrads(dx, dy, dgate, dw_post, dw_pre), None for what was not given."""
-    device = _on_gpu(x, "x")
-    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, 1.0, device)
-    p.rstd = _need(rstd, "rstd", torch.float32, (2, T), device)
+    device, index = _on_gpu(x, "x")
+    p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, 1.0, index)
+    p.rstd = _need(rstd, "rstd", torch.float32, (2, T), index)
     g = BlockNormGradParams()
-    g.dh = _need(dh, "dh", x.dtype, (T, D), device)
-    g.dn = _need(dn, "dn", torch.bfloat16, (T, D), device)
+    g.dh = _need(dh, "dh", x.dtype, (T, D), index)
+    g.dn = _need(dn, "dn", torch.bfloat16, (T, D), index)
     dx, dy, dgate, dw_post, dw_pre = torch.empty_like(x), None, None, None, None
     g.dx = dx.data_ptr()
     if y is not None:
@@ -488,15 +495,15 @@ def moe_block_norm_backward(x, y, rstd, dh, dn, *, w_post=None, gate=None, gate_
         dw_post = torch.empty_like(w_post)
         g.dw_post = dw_post.data_ptr()
     if dn is not None:
-        dw_pre = torch.empty((D,), dtype=torch.float32, device=device)
+        dw_pre = torch.empty(D, dtype=torch.float32, device=device)
         g.dw_pre = dw_pre.data_ptr()
     if ws is None:
         ws = torch.empty(block_norm_backward_ws_bytes(T, D), dtype=torch.uint8, device=device)
-    _call("moe_block_norm_backward", device, p, g, _need(ws, "ws", torch.uint8, ws.shape, device), ws.numel())
+    _call("moe_block_norm_backward", index, p, g, _need(ws, "ws", torch.uint8, ws.shape, index), ws.numel())
     return BlockNormGrads(dx, dy, dgate, dw_post, dw_pre)
 
 
-def _router_params(logits, topk, score, renorm, scale, bias, valid, device):
+def _router_params(logits, topk, score, renorm, scale, bias, valid, index):
     if logits.dim() != 2 or logits.dtype not in _ROW_TYPES:
         raise ValueError(f"logits: need a bfloat16 or float32 tensor [tokens, experts], got {logits.dtype} of "
                          f"{tuple(logits.shape)}")
@@ -505,9 +512,9 @@ def _router_params(logits, topk, score, renorm, scale, bias, valid, device):
         valid = valid.view(torch.uint8)
     r = RouterParams(tokens=T, num_experts=E, topk=topk, dt=_ROW_TYPES[logits.dtype],
                      score=_pick(SCORES, score, "score"), renorm=int(bool(renorm)), scale=scale)
-    r.logits = _need(logits, "logits", logits.dtype, (T, E), device)
-    r.bias = _need(bias, "bias", torch.float32, (E,), device)
-    r.valid = _need(valid, "valid", torch.uint8, (T,), device)
+    r.logits = _need(logits, "logits", logits.dtype, (T, E), index)
+    r.bias = _need(bias, "bias", torch.float32, (E,), index)
+    r.valid = _need(valid, "valid", torch.uint8, (T,), index)
     return r, T, E
 
 
@@ -519,21 +526,21 @@ def moe_router(logits, topk, *, score="softmax", renorm=True, scale=1.0, bias=No
 
     Returns Routing(ids int32 [T, topk], w fp32 [T, topk], balance), balance being None or
     Balance(counts, mean_prob, loss [2], num_valid, coef, z_coef)."""
-    device = _on_gpu(logits, "logits")
-    r, T, E = _router_params(logits, topk, score, renorm, scale, bias, valid, device)
-    ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=device)
-    w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=device)
+    device, index = _on_gpu(logits, "logits")
+    r, T, E = _router_params(logits, topk, score, renorm, scale, bias, valid, index)
+    ids = torch.empty(T, max(topk, 0), dtype=torch.int32, device=device)
+    w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=device)
     r.topk_ids, r.topk_w = ids.data_ptr(), w.data_ptr()
     if balance is None:
-        _call("moe_router", device, r, None, None, 0)
+        _call("moe_router", index, r, None, None, 0)
         return Routing(ids, w, None)
     coef, z_coef = balance
-    b = Balance(torch.empty((E,), dtype=torch.int32, device=device), torch.empty((E,), dtype=torch.float32, device=device),
-                torch.empty((2,), dtype=torch.float32, device=device), torch.empty((1,), dtype=torch.int32, device=device),
+    b = Balance(torch.empty(E, dtype=torch.int32, device=device), torch.empty(E, dtype=torch.float32, device=device),
+                torch.empty(2, dtype=torch.float32, device=device), torch.empty(1, dtype=torch.int32, device=device),
                 coef, z_coef)
     if ws is None:
         ws = torch.empty(router_ws_bytes(E), dtype=torch.uint8, device=device)
-    _call("moe_router", device, r, _balance_params(b), _need(ws, "ws", torch.uint8, ws.shape, device), ws.numel())
+    _call("moe_router", index, r, _balance_params(b), _need(ws, "ws", torch.uint8, ws.shape, index), ws.numel())
     return Routing(ids, w, b)
 
 
@@ -546,49 +553,49 @@ def moe_router_backward(logits, routing, d_w=None, *, d_loss=None, score="softma
     """d_logits of moe_router, given its result: from d_w (fp32 [T, topk], gradient of the weights) and,
     where it took the balance statistics, d_loss (fp32 [2] on the GPU, gradients of the two losses;
     None for ones).  The other arguments as in the forward call."""
-    device = _on_gpu(logits, "logits")
+    device, index = _on_gpu(logits, "logits")
     if routing.ids.dim() != 2:
         raise ValueError(f"routing.ids: need [tokens, topk], got {tuple(routing.ids.shape)}")
     topk = routing.ids.shape[1]
-    r, T, E = _router_params(logits, topk, score, renorm, scale, None, valid, device)
-    r.topk_ids = _need(routing.ids, "routing.ids", torch.int32, (T, topk), device)
+    r, T, E = _router_params(logits, topk, score, renorm, scale, None, valid, index)
+    r.topk_ids = _need(routing.ids, "routing.ids", torch.int32, (T, topk), index)
     b = routing.balance
     if b is not None:
-        _need(b.counts, "balance.counts", torch.int32, (E,), device)
-        _need(b.num_valid, "balance.num_valid", torch.int32, (1,), device)
+        _need(b.counts, "balance.counts", torch.int32, (E,), index)
+        _need(b.num_valid, "balance.num_valid", torch.int32, (1,), index)
         b = _balance_params(b)
     d_logits = torch.empty_like(logits)
-    _call("moe_router_backward", device, r, b, _need(d_w, "d_w", torch.float32, (T, topk), device),
-          _need(d_loss, "d_loss", torch.float32, (2,), device), d_logits.data_ptr())
+    _call("moe_router_backward", index, r, b, _need(d_w, "d_w", torch.float32, (T, topk), index),
+          _need(d_loss, "d_loss", torch.float32, (2,), index), d_logits.data_ptr())
     return d_logits
 
 
 def moe_quant_i8(x, q=None, scale=None):
     """bf16 [rows, cols] -> (int8 codes, fp32 scale per row), see moe_quant_i8 in the header."""
-    device = _on_gpu(x, "x")
+    device, index = _on_gpu(x, "x")
     if x.dim() != 2:
         raise ValueError(f"x: need [rows, cols], got {tuple(x.shape)}")
     rows, cols = x.shape
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.int8, device=device)
+        q = torch.empty(rows, cols, dtype=torch.int8, device=device)
     if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=device)
-    _call("moe_quant_i8", device, _need(x, "x", torch.bfloat16, (rows, cols), device), rows, cols,
-          _need(q, "q", torch.int8, (rows, cols), device), _need(scale, "scale", torch.float32, (rows,), device))
+        scale = torch.empty(rows, dtype=torch.float32, device=device)
+    _call("moe_quant_i8", index, _need(x, "x", torch.bfloat16, (rows, cols), index), rows, cols,
+          _need(q, "q", torch.int8, (rows, cols), index), _need(scale, "scale", torch.float32, (rows,), index))
     return q, scale
 
 
 def moe_pack_i8(w, out=None):
     """int8 weights [out_features, in_features] -> the packed layout moe_gemm_i8 reads."""
-    device = _on_gpu(w, "w")
+    device, index = _on_gpu(w, "w")
     if w.dim() != 2:
         raise ValueError(f"w: need [out_features, in_features], got {tuple(w.shape)}")
     N, K = w.shape
     shape = i8_packed_shape(N, K)
     if out is None:
         out = torch.empty(shape, dtype=torch.int8, device=device)
-    _call("moe_pack_i8", device, _need(w, "w", torch.int8, (N, K), device), N, K,
-          _need(out, "out", torch.int8, shape, device))
+    _call("moe_pack_i8", index, _need(w, "w", torch.int8, (N, K), index), N, K,
+          _need(out, "out", torch.int8, shape, index))
     return out
 
 
@@ -596,7 +603,7 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
     """int8 tokens [T, K] (scales [T]) times packed int8 weights of w_scale.numel() rows -> bf16, with
     act "situv2" or "silu" of the [gate|up] halves and `add` (bf16, shape of the result) in the same
     launch (see moe_gemm_i8 in the header)."""
-    device = _on_gpu(a, "a")
+    device, index = _on_gpu(a, "a")
     if a.dim() != 2 or w_scale.dim() != 1:
         raise ValueError(f"need a [tokens, in_features] and w_scale [out_features], got {tuple(a.shape)} and "
                          f"{tuple(w_scale.shape)}")
@@ -610,10 +617,10 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
         params = ActParams(k, 0.0 if beta is None else beta, 0.0 if linear_beta is None else linear_beta)
     shape = (T, N if act is None else N // 2)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    _call("moe_gemm_i8", device, _need(a, "a", torch.int8, (T, K), device),
-          _need(a_scale, "a_scale", torch.float32, (T,), device),
-          _need(w_packed, "w_packed", torch.int8, i8_packed_shape(N, K), device),
-          _need(w_scale, "w_scale", torch.float32, (N,), device), T, N, K, params,
-          _need(add, "add", torch.bfloat16, shape, device), _need(out, "out", torch.bfloat16, shape, device))
+        out = torch.empty(*shape, dtype=torch.bfloat16, device=device)
+    _call("moe_gemm_i8", index, _need(a, "a", torch.int8, (T, K), index),
+          _need(a_scale, "a_scale", torch.float32, (T,), index),
+          _need(w_packed, "w_packed", torch.int8, i8_packed_shape(N, K), index),
+          _need(w_scale, "w_scale", torch.float32, (N,), index), T, N, K, params,
+          _need(add, "add", torch.bfloat16, shape, index), _need(out, "out", torch.bfloat16, shape, index))
     return out

@@ -183,7 +183,7 @@ def test_binding_refuses_tensors_off_the_gpu_and_unknown_names():
                  lambda: qm.moe_pack_i8(x), lambda: qm.moe_gemm_i8(x, None, None, None)):
         with pytest.raises(ValueError, match="on the GPU"):
             call()
-    dev = x.device
+    dev = -1                                                   # the index of a tensor on the CPU
     with pytest.raises(ValueError, match="gate_kind"):
         qm._norm_params(x, None, None, None, "row", "none", 1.0, None, 1e-6, dev)
     with pytest.raises(ValueError, match="go together"):
