@@ -17,11 +17,22 @@
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
+#include <initializer_list>
+#include <type_traits>
+
 namespace moe {
 
 namespace {
 
 constexpr int MAX_W = 16;                     // waves of a row, at most
+
+// Element `i` of a row whose address is wave-uniform: one 32-bit offset per lane serves every row
+// (64-bit addresses per lane and row took more registers than the data).
+template <class T>
+__device__ __forceinline__ T* el(T* row, int i) {
+  typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
+  return reinterpret_cast<T*>(reinterpret_cast<byte*>(row) + (uint32_t)(i * (int)sizeof(T)));
+}
 
 // Sums over a row of W waves of NV values; buf is this reduction's own NV * MAX_W floats.
 template <int NV>
@@ -54,21 +65,38 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, float* buf, int W) {
   return row16_max_u32((lane & 15) < W ? __float_as_uint(buf[lane & 15]) : 0u);
 }
 
-__device__ __forceinline__ float gate_value(float g, int act) {
-  return act == MOE_GATE_SIGMOID ? fast_sigmoid(g) : g;
+// 1 / sqrt(v): the hardware's estimate (1 ulp) and one Newton step.  An error here moves a whole row,
+// and with it every code of the row that is near a border.
+__device__ __forceinline__ float rsqrt_f(float v) {
+  const float r = __builtin_amdgcn_rsqf(v);
+  const float e = __builtin_fmaf(-v * r, r, 1.0f);
+  return r > 0.0f && r < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
+}
+// sigmoid with the rounding of the exponent's product and of the reciprocal taken back (2 ulp)
+__device__ __forceinline__ float sigmoid_f(float x) {
+  constexpr float L2E = 1.4426950408889634f, L2E_LOW = 1.92596299e-8f;
+  const float t = __builtin_fminf(-L2E * x, 126.0f);
+  const float low = __builtin_fmaf(-L2E, x, -t) - L2E_LOW * x;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float d = 1.0f + (t < 126.0f ? __builtin_fmaf(e, low * 0.6931472f, e) : e);
+  const float r = __builtin_amdgcn_rcpf(d);
+  return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }
 
-// The gate of this lane's VEC elements (columns from `col`), before its activation; ones without one.
-template <int VEC>
-__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t at, int col, float token_gate, float (&g)[VEC]) {
-  if (a.gate_kind == MOE_GATE_CHANNEL) {
-    load_row<VEC>(static_cast<const float*>(a.gate) + col, g);
-  } else if (a.gate_kind == MOE_GATE_ELEMENT) {
-    load_row<VEC>(static_cast<const uint16_t*>(a.gate) + at, g);
-  } else {
+// The gate of this lane's VEC elements after its activation (GATE: what it is shared by).
+// row_gate: the row's gate with MOE_GATE_TOKEN.
+template <int GATE, int VEC>
+__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t base, int col, float row_gate, float (&g)[VEC]) {
+  if constexpr (GATE == MOE_GATE_CHANNEL) load_row<VEC>(el(static_cast<const float*>(a.gate), col), g);
+  if constexpr (GATE == MOE_GATE_ELEMENT) load_row<VEC>(el(static_cast<const uint16_t*>(a.gate) + base, col), g);
+  g[0] = GATE == MOE_GATE_NONE ? 1.0f : GATE == MOE_GATE_TOKEN ? row_gate : g[0];
+  constexpr int n = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_ELEMENT ? VEC : 1;   // distinct values
+  if (GATE != MOE_GATE_NONE && a.gate_act == MOE_GATE_SIGMOID) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) g[j] = token_gate;          // MOE_GATE_TOKEN, or 1
+    for (int j = 0; j < n; ++j) g[j] = sigmoid_f(g[j]);
   }
+#pragma unroll
+  for (int j = n; j < VEC; ++j) g[j] = g[0];
 }
 
 // Codes of VEC = 8 consecutive elements; four adjacent lanes hold a block of 32 (inactive lanes
@@ -102,64 +130,66 @@ __device__ __forceinline__ void store_mx(const float (&v)[8], const NormArgs& a,
 
 // One row per W waves; R = blockDim.x / (64 W) rows per workgroup (R > 1 only with W == 1, so no
 // barrier is ever reached by part of a workgroup).
-template <int VEC, int CH, class XT>
+template <int VEC, int CH, int GATE, class XT>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
   __shared__ float red[3][MAX_W];
   const int tr = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : blockIdx.x;
+  const int sub = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + sub : blockIdx.x;
   if (row >= a.T) return;
   const int64_t base = row * a.D;
   const XT* const x = static_cast<const XT*>(a.x);
   const float inv_d = 1.0f / (float)a.D;
-  float h[CH][VEC];
+  // Lanes past the row read its last elements again and hold zeros: loads without branches, all of
+  // them in flight together.
+  float h[CH][VEC], y[CH][VEC];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int col = (c * W * 64 + tr) * VEC;
-    if (col < a.D) {
-      load_row<VEC>(x + base + col, h[c]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) h[c][j] = 0.0f;
-    }
-  }
+  for (int c = 0; c < CH; ++c) load_row<VEC>(el(x + base, min((c * W * 64 + tr) * VEC, a.D - VEC)), h[c]);
   if (a.y) {
-    float y[CH][VEC];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) load_row<VEC>(el(a.y + base, min((c * W * 64 + tr) * VEC, a.D - VEC)), y[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < CH; ++c)
+    if ((c * W * 64 + tr) * VEC >= a.D) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) h[c][j] = y[c][j] = 0.0f;
+    }
+  if (a.y) {
     float s[1] = {0.0f};
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * W * 64 + tr) * VEC;
-      if (col < a.D) {
-        load_row<VEC>(a.y + base + col, y[c]);
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s[0] += y[c][j] * y[c][j];
-      }
-    }
+      for (int j = 0; j < VEC; ++j) s[0] += y[c][j] * y[c][j];
     float ry = 1.0f;
     if (a.w_post) {
       row_sums<1>(s, red[0], W);
-      ry = __builtin_amdgcn_rsqf(s[0] * inv_d + a.eps);
+      ry = rsqrt_f(s[0] * inv_d + a.eps);
       if (a.rstd && tr == 0) a.rstd[row] = ry;
     }
-    const float token_gate = a.gate_kind == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    const float row_gate = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
     const float k = a.scale * ry;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * W * 64 + tr) * VEC;
       if (col < a.D) {
         float g[VEC], w[VEC];
-        load_gate<VEC>(a, base + col, col, token_gate, g);
-        if (a.w_post) load_row<VEC>(a.w_post + col, w);
+        load_gate<GATE, VEC>(a, base, col, row_gate, g);
+        if (a.w_post) {
+          load_row<VEC>(el(a.w_post, col), w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          h[c][j] += k * gate_value(g[j], a.gate_act) * (a.w_post ? y[c][j] * w[j] : y[c][j]);
-        if (a.h) store_row<VEC>(static_cast<XT*>(a.h) + base + col, h[c]);
+          for (int j = 0; j < VEC; ++j) y[c][j] *= w[j];
+        }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) h[c][j] += k * g[j] * y[c][j];
+        if (a.h) store_row<VEC>(el(static_cast<XT*>(a.h) + base, col), h[c]);
       }
     }
   } else if (a.h) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * W * 64 + tr) * VEC;
-      if (col < a.D) store_row<VEC>(static_cast<XT*>(a.h) + base + col, h[c]);
+      if (col < a.D) store_row<VEC>(el(static_cast<XT*>(a.h) + base, col), h[c]);
     }
   }
   if (!a.w_pre) return;
@@ -169,7 +199,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s[0] += h[c][j] * h[c][j];
   row_sums<1>(s, red[1], W);
-  const float rh = __builtin_amdgcn_rsqf(s[0] * inv_d + a.eps);
+  const float rh = rsqrt_f(s[0] * inv_d + a.eps);
   if (a.rstd && tr == 0) a.rstd[a.T + row] = rh;
   uint32_t amax = 0;
 #pragma unroll
@@ -178,10 +208,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
     const bool active = col < a.D;
     if (active) {
       float w[VEC];
-      load_row<VEC>(a.w_pre + col, w);
+      load_row<VEC>(el(a.w_pre, col), w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[c][j] = h[c][j] * rh * w[j];
-      if (a.n) store_row<VEC>(a.n + base + col, h[c]);
+      if (a.n) store_row<VEC>(el(a.n + base, col), h[c]);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[c][j] = 0.0f;
@@ -205,7 +235,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
           uint32_t q[2] = {0, 0};
 #pragma unroll
           for (int j = 0; j < VEC; ++j) q[j / 4] |= rs.code(h[c][j]) << (8 * (j % 4));
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.q) + base + col) = uint2{q[0], q[1]};
+          *reinterpret_cast<uint2*>(el(static_cast<uint8_t*>(a.q) + base, col)) = uint2{q[0], q[1]};
         }
       }
     }
@@ -214,69 +244,79 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
 
 // Rows blockIdx.x * R + sub, then every gridDim.x * R rows.  Each (workgroup, sub) writes one
 // partial row of the three sums over rows: [dw_pre | dw_post | dgate (per channel)].
-template <int VEC, int CH, class XT>
+template <int VEC, int CH, int GATE, class XT>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardArgs b, int W) {
   __shared__ float red[2][2][2 * MAX_W];
   const NormArgs& a = b.f;
-  const int R = W == 1 ? blockDim.x >> 6 : 1, sub = W == 1 ? threadIdx.x >> 6 : 0;
+  const int R = W == 1 ? blockDim.x >> 6 : 1, sub = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
   const int tr = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   const float inv_d = 1.0f / (float)a.D;
   const XT* const x = static_cast<const XT*>(a.x);
-  const bool token = a.gate_kind == MOE_GATE_TOKEN, element = a.gate_kind == MOE_GATE_ELEMENT;
-  float acc_pre[CH][VEC], acc_post[CH][VEC], acc_gate[CH][VEC];
+  const bool has_y = a.y != nullptr, post = a.w_post != nullptr, has_dn = b.dn != nullptr, has_dh = b.dh != nullptr;
+  const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
+  constexpr bool fixed_gate = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_NONE;
+  float acc_pre[CH][VEC], acc_post[CH][VEC], acc_gate[CH][VEC], g[CH][VEC];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+  for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc_pre[c][j] = acc_post[c][j] = acc_gate[c][j] = 0.0f;
+    if constexpr (fixed_gate) load_gate<GATE, VEC>(a, 0, min((c * W * 64 + tr) * VEC, a.D - VEC), 1.0f, g[c]);
+  }
   int parity = 0;
   for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.T; row += (int64_t)gridDim.x * R, parity ^= 1) {
     const int64_t base = row * a.D;
-    const float ry = a.w_post ? a.rstd[row] : 1.0f;
-    const float token_gate = token ? static_cast<const float*>(a.gate)[row] : 1.0f;
-    float h[CH][VEC], y[CH][VEC], g[CH][VEC], u[CH][VEC], e[CH][VEC];
+    // opaque, so that the compiler keeps one 32-bit offset instead of a 64-bit address per array and chunk
+    int lane_at = tr * VEC;
+    asm volatile("" : "+v"(lane_at));
+    const float ry = post ? a.rstd[row] : 1.0f;
+    const float rh = has_dn ? a.rstd[a.T + row] : 0.0f;
+    const float row_gate = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    float h[CH][VEC], y[CH][VEC], u[CH][VEC], e[CH][VEC];
+    // as in the forward pass: loads without branches on the lane, all in flight together; lanes past
+    // the row hold zeros in h, y, u and e
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = min(c * W * 64 * VEC + lane_at, a.D - VEC);
+      load_row<VEC>(el(x + base, at), h[c]);
+      if (has_y) load_row<VEC>(el(a.y + base, at), y[c]);
+      if (has_dn) load_row<VEC>(el(b.dn + base, at), u[c]);
+      if (has_dh) load_row<VEC>(el(static_cast<const XT*>(b.dh) + base, at), e[c]);
+      if constexpr (!fixed_gate) load_gate<GATE, VEC>(a, base, at, row_gate, g[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const bool out = c * W * 64 * VEC + lane_at >= a.D;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        h[c][j] = out ? 0.0f : h[c][j];
+        y[c][j] = out || !has_y ? 0.0f : y[c][j] * ry;        // yh (y itself without w_post)
+        u[c][j] = out || !has_dn ? 0.0f : u[c][j];
+        e[c][j] = out || !has_dh ? 0.0f : e[c][j];
+      }
+    }
     float s1[1] = {0.0f};
-    const float rh = a.w_pre ? a.rstd[a.T + row] : 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * W * 64 + tr) * VEC;
+      const int at = min(c * W * 64 * VEC + lane_at, a.D - VEC);
+      if (has_y) {
+        float w[VEC];
+        if (post) load_row<VEC>(el(a.w_post, at), w);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) h[c][j] = y[c][j] = g[c][j] = u[c][j] = e[c][j] = 0.0f;
-      if (col < a.D) {
-        load_row<VEC>(x + base + col, h[c]);
-        if (a.y) {
-          load_row<VEC>(a.y + base + col, y[c]);
-          load_gate<VEC>(a, base + col, col, token_gate, g[c]);
-        }
-        if (b.dn) load_row<VEC>(b.dn + base + col, u[c]);
-        if (b.dh) load_row<VEC>(static_cast<const XT*>(b.dh) + base + col, e[c]);
+        for (int j = 0; j < VEC; ++j) h[c][j] += a.scale * g[c][j] * (post ? y[c][j] * w[j] : y[c][j]);
       }
-    }
+      if (has_dn) {
+        float v[VEC];
+        load_row<VEC>(el(a.w_pre, at), v);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = (c * W * 64 + tr) * VEC;
-      if (col < a.D) {
-        float w[VEC], v[VEC];
-        if (a.y) {
-          if (a.w_post) load_row<VEC>(a.w_post + col, w);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            y[c][j] *= ry;                                    // yh (y itself without w_post)
-            h[c][j] += a.scale * gate_value(g[c][j], a.gate_act) * (a.w_post ? y[c][j] * w[j] : y[c][j]);
-          }
-        }
-        if (b.dn) {
-          load_row<VEC>(a.w_pre + col, v);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            h[c][j] *= rh;                                    // hh
-            acc_pre[c][j] += u[c][j] * h[c][j];
-            u[c][j] *= v[j];
-            s1[0] += u[c][j] * h[c][j];
-          }
+        for (int j = 0; j < VEC; ++j) {
+          h[c][j] *= rh;                                      // hh
+          acc_pre[c][j] += u[c][j] * h[c][j];
+          u[c][j] *= v[j];
+          s1[0] += u[c][j] * h[c][j];
         }
       }
     }
-    if (b.dn) {
+    if (has_dn) {
       row_sums<1>(s1, red[parity][0], W);
       const float m = s1[0] * inv_d;
 #pragma unroll
@@ -286,44 +326,47 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int col = (c * W * 64 + tr) * VEC;
-      if (col < a.D) store_row<VEC>(static_cast<XT*>(b.dx) + base + col, e[c]);
+      const int col = c * W * 64 * VEC + lane_at;
+      if (col < a.D) store_row<VEC>(el(static_cast<XT*>(b.dx) + base, col), e[c]);
     }
-    if (a.y) {
-      float s2[2] = {0.0f, 0.0f};
+    if (!has_y) continue;
+    float s2[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = (c * W * 64 + tr) * VEC;
-        if (col < a.D) {
-          float w[VEC], dg[VEC];
-          if (a.w_post) load_row<VEC>(a.w_post + col, w);
+    for (int c = 0; c < CH; ++c) {
+      const int col = c * W * 64 * VEC + lane_at;
+      float w[VEC], dg[VEC];
+      if (post) load_row<VEC>(el(a.w_post, min(col, a.D - VEC)), w);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float gv = gate_value(g[c][j], a.gate_act);
-            const float se = a.scale * e[c][j];
-            const float z = a.w_post ? y[c][j] * w[j] : y[c][j];
-            dg[j] = se * z * (a.gate_act == MOE_GATE_SIGMOID ? gv * (1.0f - gv) : 1.0f);
-            const float dz = se * gv;
-            u[c][j] = a.w_post ? dz * w[j] : dz;
-            acc_post[c][j] += dz * y[c][j];
-            acc_gate[c][j] += dg[j];
-            s2[0] += u[c][j] * y[c][j];
-            s2[1] += dg[j];
-          }
-          if (element) store_row<VEC>(static_cast<uint16_t*>(b.dgate) + base + col, dg);
+      for (int j = 0; j < VEC; ++j) {
+        const float se = a.scale * e[c][j];
+        const float dz = se * g[c][j];
+        u[c][j] = post ? dz * w[j] : dz;
+        acc_post[c][j] += dz * y[c][j];
+        s2[0] += u[c][j] * y[c][j];
+        if constexpr (GATE != MOE_GATE_NONE) {
+          dg[j] = se * (post ? y[c][j] * w[j] : y[c][j]);
+          if (sigmoid) dg[j] *= g[c][j] * (1.0f - g[c][j]);
+          if constexpr (GATE == MOE_GATE_CHANNEL) acc_gate[c][j] += dg[j];
+          if constexpr (GATE == MOE_GATE_TOKEN) s2[1] += dg[j];
         }
       }
-      if (a.w_post || token) row_sums<2>(s2, red[parity][1], W);
-      if (token && tr == 0) static_cast<float*>(b.dgate)[row] = s2[1];
-      const float m = a.w_post ? s2[0] * inv_d : 0.0f;
+      if constexpr (GATE == MOE_GATE_ELEMENT)
+        if (col < a.D) store_row<VEC>(el(static_cast<uint16_t*>(b.dgate) + base, col), dg);
+    }
+    if constexpr (GATE == MOE_GATE_TOKEN) {
+      row_sums<2>(s2, red[parity][1], W);
+      if (tr == 0) static_cast<float*>(b.dgate)[row] = s2[1];
+    } else if (post) {
+      row_sums<1>(reinterpret_cast<float(&)[1]>(s2), red[parity][1], W);
+    }
+    const float m = post ? s2[0] * inv_d : 0.0f;
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int col = (c * W * 64 + tr) * VEC;
-        if (col < a.D) {
+    for (int c = 0; c < CH; ++c) {
+      const int col = c * W * 64 * VEC + lane_at;
+      if (col < a.D) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) u[c][j] = ry * (u[c][j] - y[c][j] * m);
-          store_row<VEC>(b.dy + base + col, u[c]);
-        }
+        for (int j = 0; j < VEC; ++j) u[c][j] = ry * (u[c][j] - y[c][j] * m);
+        store_row<VEC>(el(b.dy + base, col), u[c]);
       }
     }
   }
@@ -334,24 +377,25 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     if (col < a.D) {
       if (b.dw_pre) store_row<VEC>(part + col, acc_pre[c]);
       if (b.dw_post) store_row<VEC>(part + a.D + col, acc_post[c]);
-      if (a.gate_kind == MOE_GATE_CHANNEL) store_row<VEC>(part + 2 * (int64_t)a.D + col, acc_gate[c]);
+      if constexpr (GATE == MOE_GATE_CHANNEL) store_row<VEC>(part + 2 * (int64_t)a.D + col, acc_gate[c]);
     }
   }
 }
 
 // out_k[col] = sum over the partial rows, for the sums that are asked for (blockIdx.y = k).
-// 16 columns x 16 row classes per workgroup; every class adds its rows in order, then the
-// classes are added in order.
-__global__ __launch_bounds__(256) void norm_sum_parts_kernel(const float* __restrict__ part, int nparts, int D,
-                                                             float* dw_pre, float* dw_post, float* dgate) {
+// 64 columns x 16 row classes per workgroup; every class adds its rows in order, then the
+// classes are added in order.  (16 columns x 16 classes took 12 us for 512 x 3 x 3584.)
+__global__ __launch_bounds__(1024) void norm_sum_parts_kernel(const float* __restrict__ part, int nparts, int D,
+                                                              float* dw_pre, float* dw_post, float* dgate) {
   float* const out = blockIdx.y == 0 ? dw_pre : blockIdx.y == 1 ? dw_post : dgate;
   if (!out) return;
-  __shared__ float lds[16][17];
-  const int cl = threadIdx.x & 15, rc = threadIdx.x >> 4;
-  const int col = blockIdx.x * 16 + cl;
+  __shared__ float lds[16][64];
+  const int cl = threadIdx.x & 63, rc = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + cl;
+  const float* const src = part + (int64_t)blockIdx.y * D + min(col, D - 1);
   float s = 0.0f;
-  if (col < D)
-    for (int p = rc; p < nparts; p += 16) s += part[((int64_t)p * 3 + blockIdx.y) * D + col];
+#pragma unroll 8
+  for (int p = rc; p < nparts; p += 16) s += src[(int64_t)p * 3 * D];
   lds[rc][cl] = s;
   __syncthreads();
   if (rc == 0 && col < D) {
@@ -360,72 +404,87 @@ __global__ __launch_bounds__(256) void norm_sum_parts_kernel(const float* __rest
   }
 }
 
-// Whether every row of every given tensor can be read 16 bytes at a time.
-bool aligned16(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if ((uintptr_t)p & 15) return false;
-  return true;
-}
-
+// Elements per lane and access (8 where rows and pointers allow it, 2 in rows of even width, else
+// 1), in as few chunks as 16 waves hold.
 struct Shape { int vec, ch, W, threads, R; };
-// 8 elements per lane where rows and pointers allow it (else one), in as few chunks as 16 waves hold.
-Shape norm_shape(int D, bool wide) {
+Shape norm_shape(int D, int vec) {
   Shape s;
-  s.vec = wide ? 8 : 1;
-  const int per_wave = 64 * s.vec;
-  s.ch = wide ? (D > MAX_W * per_wave ? 2 : 1) : (D > 4 * MAX_W * per_wave ? 16 : 4);
+  s.vec = vec;
+  const int per_wave = 64 * vec;
+  const int few = vec == 8 ? 1 : 4;
+  s.ch = D <= few * MAX_W * per_wave ? few : vec == 8 ? 2 : vec == 2 ? 8 : 16;
   s.W = (D + per_wave * s.ch - 1) / (per_wave * s.ch);
   s.R = s.W == 1 ? 4 : 1;
   s.threads = 64 * s.W * s.R;
   return s;
 }
 
-template <class XT>
-void norm_forward(const NormArgs& a, const Shape& sh, hipStream_t s) {
-  const unsigned grid = (unsigned)((a.T + sh.R - 1) / sh.R);
-  if (sh.vec == 8 && sh.ch == 1) norm_kernel<8, 1, XT><<<grid, sh.threads, 0, s>>>(a, sh.W);
-  else if (sh.vec == 8) norm_kernel<8, 2, XT><<<grid, sh.threads, 0, s>>>(a, sh.W);
-  else if (sh.ch == 4) norm_kernel<1, 4, XT><<<grid, sh.threads, 0, s>>>(a, sh.W);
-  else norm_kernel<1, 16, XT><<<grid, sh.threads, 0, s>>>(a, sh.W);
+// f(VEC, CH, GATE as integral constants, a value of the residual stream's type)
+template <int V>
+using Const = std::integral_constant<int, V>;
+template <int VEC, int CH, class F>
+void norm_typed(const NormArgs& a, const F& f) {
+  const auto typed = [&](auto xt) {
+    switch (a.gate_kind) {
+      case MOE_GATE_CHANNEL: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_CHANNEL>(), xt); break;
+      case MOE_GATE_TOKEN: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_TOKEN>(), xt); break;
+      case MOE_GATE_ELEMENT: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_ELEMENT>(), xt); break;
+      default: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_NONE>(), xt); break;
+    }
+  };
+  if (a.x_dt == MOE_DT_F32) typed(float());
+  else typed(uint16_t());
+}
+template <class F>
+void norm_dispatch(const NormArgs& a, const Shape& sh, const F& f) {
+  if (sh.vec == 8) {
+    if (sh.ch == 1) norm_typed<8, 1>(a, f);
+    else norm_typed<8, 2>(a, f);
+  } else if (sh.vec == 2) {
+    if (sh.ch == 4) norm_typed<2, 4>(a, f);
+    else norm_typed<2, 8>(a, f);
+  } else {
+    if (sh.ch == 4) norm_typed<1, 4>(a, f);
+    else norm_typed<1, 16>(a, f);
+  }
 }
 
-template <class XT>
-void norm_backward(const NormBackwardArgs& b, const Shape& sh, unsigned grid, hipStream_t s) {
-  if (sh.vec == 8 && sh.ch == 1) norm_backward_kernel<8, 1, XT><<<grid, sh.threads, 0, s>>>(b, sh.W);
-  else if (sh.vec == 8) norm_backward_kernel<8, 2, XT><<<grid, sh.threads, 0, s>>>(b, sh.W);
-  else if (sh.ch == 4) norm_backward_kernel<1, 4, XT><<<grid, sh.threads, 0, s>>>(b, sh.W);
-  else norm_backward_kernel<1, 16, XT><<<grid, sh.threads, 0, s>>>(b, sh.W);
+// The widest access that rows of D elements of every given tensor allow.
+int norm_vec(int D, std::initializer_list<const void*> ps) {
+  uintptr_t bits = 0;
+  for (const void* p : ps) bits |= (uintptr_t)p;
+  return D % 8 == 0 && !(bits & 15) ? 8 : D % 2 == 0 && !(bits & 7) ? 2 : 1;
 }
-
 const void* wide_gate(const NormArgs& a) { return a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate; }
 
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
-  const bool wide = a.D % 8 == 0 && aligned16({a.x, a.y, a.w_post, wide_gate(a), a.w_pre, a.h, a.n, a.q});
-  const Shape sh = norm_shape(a.D, wide);
-  if (a.x_dt == MOE_DT_F32) norm_forward<float>(a, sh, s);
-  else norm_forward<uint16_t>(a, sh, s);
+  const Shape sh = norm_shape(a.D, norm_vec(a.D, {a.x, a.y, a.w_post, wide_gate(a), a.w_pre, a.h, a.n, a.q}));
+  const unsigned grid = (unsigned)((a.T + sh.R - 1) / sh.R);
+  norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto xt) {
+    norm_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, sh.threads, 0, s>>>(a, sh.W);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_block_norm_backward(const NormBackwardArgs& b, hipStream_t s) {
   const NormArgs& a = b.f;
-  const bool wide = a.D % 8 == 0 && aligned16({a.x, a.y, a.w_post, wide_gate(a), a.w_pre, b.dh, b.dn, b.dx, b.dy,
-                                               a.gate_kind == MOE_GATE_ELEMENT ? b.dgate : nullptr, b.part});
-  const Shape sh = norm_shape(a.D, wide);
+  const Shape sh = norm_shape(a.D, norm_vec(a.D, {a.x, a.y, a.w_post, wide_gate(a), a.w_pre, b.dh, b.dn, b.dx, b.dy,
+                                                  a.gate_kind == MOE_GATE_ELEMENT ? b.dgate : nullptr, b.part}));
   const int groups = (a.T + sh.R - 1) / sh.R, most = MOE_NORM_PARTS / sh.R;
   const unsigned grid = (unsigned)(groups < most ? groups : most);
   if (grid > 0) {                                             // no rows: the sums below are zero
-    if (a.x_dt == MOE_DT_F32) norm_backward<float>(b, sh, grid, s);
-    else norm_backward<uint16_t>(b, sh, grid, s);
+    norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto xt) {
+      norm_backward_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, sh.threads, 0, s>>>(b, sh.W);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   float* const dgate = a.gate_kind == MOE_GATE_CHANNEL ? static_cast<float*>(b.dgate) : nullptr;
   if (!b.dw_pre && !b.dw_post && !dgate) return hipSuccess;
-  norm_sum_parts_kernel<<<dim3((unsigned)((a.D + 15) / 16), 3), 256, 0, s>>>(b.part, (int)grid * sh.R, a.D, b.dw_pre,
-                                                                            b.dw_post, dgate);
+  norm_sum_parts_kernel<<<dim3((unsigned)((a.D + 63) / 64), 3), 1024, 0, s>>>(b.part, (int)grid * sh.R, a.D, b.dw_pre,
+                                                                             b.dw_post, dgate);
   return hipGetLastError();
 }
 
