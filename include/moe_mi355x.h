@@ -368,7 +368,7 @@ typedef enum { MOE_GATE_RAW = 0, MOE_GATE_SIGMOID = 1 } moe_gate_act_t;
 /* Widest row of moe_block_norm. */
 #define MOE_NORM_MAX_DIM 16384
 /* Most partial sums of moe_block_norm_backward. */
-#define MOE_NORM_PARTS 512
+#define MOE_NORM_PARTS 256
 
 typedef struct {
   const void *x;        /* [tokens, dim] residual stream, bf16 or fp32 (x_dt) */
@@ -420,7 +420,7 @@ typedef struct {
 /* Workspace of moe_block_norm_backward: one row of partial sums per workgroup for each of dw_pre,
  * dw_post and a per-channel gate. */
 static inline size_t moe_block_norm_backward_ws_bytes(int32_t tokens, int32_t dim) {
-  size_t parts = tokens < MOE_NORM_PARTS ? ((size_t)(tokens > 0 ? tokens : 0) + 3) / 4 * 4 : MOE_NORM_PARTS;
+  size_t parts = tokens < MOE_NORM_PARTS ? (size_t)(tokens > 0 ? tokens : 0) : MOE_NORM_PARTS;
   return moe_align256(parts * 3 * (size_t)dim * 4);
 }
 

@@ -348,7 +348,7 @@ def moe_fused_noalloc(x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, topk_w, l
 # These check their tensors (type, shape, dense rows, one device) before the C call checks the
 # rest, and run on the device of their first tensor, on torch's current stream of that device.
 
-NORM_MAX_DIM, NORM_PARTS = 16384, 512
+NORM_MAX_DIM, NORM_PARTS = 16384, 256
 GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
 GATE_ACTS = {"none": 0, "sigmoid": 1}
 SCORES = {"softmax": 0, "sigmoid": 1}
@@ -363,7 +363,7 @@ Balance = collections.namedtuple("Balance", "counts mean_prob loss num_valid coe
 
 
 def block_norm_backward_ws_bytes(tokens, dim):
-    return _align256((NORM_PARTS if tokens >= NORM_PARTS else (max(tokens, 0) + 3) // 4 * 4) * 3 * dim * 4)
+    return _align256(min(max(tokens, 0), NORM_PARTS) * 3 * dim * 4)
 
 
 def router_ws_bytes(num_experts):

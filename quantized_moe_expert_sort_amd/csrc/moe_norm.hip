@@ -34,9 +34,14 @@ __device__ __forceinline__ T* el(T* row, int i) {
   return reinterpret_cast<T*>(reinterpret_cast<byte*>(row) + (uint32_t)(i * (int)sizeof(T)));
 }
 
-// Sums over a row of W waves of NV values; buf is this reduction's own NV * MAX_W floats.
+// This wave's LDS accesses are done; meet the other waves.  Only LDS is exchanged here, and
+// __syncthreads would also wait for the rows' stores.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// Sums over a row of W waves of NV values, the waves from `first` on; buf is this reduction's own
+// NV * MAX_W floats.
 template <int NV>
-__device__ __forceinline__ void row_sums(float (&v)[NV], float* buf, int W) {
+__device__ __forceinline__ void row_sums(float (&v)[NV], float* buf, int W, int first = 0) {
 #pragma unroll
   for (int k = 0; k < NV; ++k) v[k] = wave_sum(v[k]);
   if (W == 1) return;
@@ -45,10 +50,10 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* buf, int W) {
 #pragma unroll
     for (int k = 0; k < NV; ++k) buf[k * MAX_W + wave] = v[k];
   }
-  __syncthreads();
+  lds_barrier();
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    float s = (lane & 15) < W ? buf[k * MAX_W + (lane & 15)] : 0.0f;
+    float s = (lane & 15) < W ? buf[k * MAX_W + first + (lane & 15)] : 0.0f;
     s += dpp_f32<DPP_XOR1>(s);
     s += dpp_f32<DPP_XOR2>(s);
     s += dpp_f32<DPP_HALF_MIRROR>(s);
@@ -61,7 +66,7 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v, float* buf, int W) {
   if (W == 1) return v;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (lane == 0) buf[wave] = __uint_as_float(v);
-  __syncthreads();
+  lds_barrier();
   return row16_max_u32((lane & 15) < W ? __float_as_uint(buf[lane & 15]) : 0u);
 }
 
@@ -242,14 +247,15 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
   }
 }
 
-// Rows blockIdx.x * R + sub, then every gridDim.x * R rows.  Each (workgroup, sub) writes one
-// partial row of the three sums over rows: [dw_pre | dw_post | dgate (per channel)].
+// R rows at a time per workgroup, from blockIdx.x * R on, then every gridDim.x * R rows; all waves
+// make the same number of turns, so every barrier is reached by all of them.  Each workgroup
+// writes one partial row of the three sums over rows: [dw_pre | dw_post | dgate (per channel)].
 template <int VEC, int CH, int GATE, class XT>
-__global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardArgs b, int W) {
+__global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardArgs b, int W, int R) {
   __shared__ float red[2][2][2 * MAX_W];
   const NormArgs& a = b.f;
-  const int R = W == 1 ? blockDim.x >> 6 : 1, sub = W == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
-  const int tr = W == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int sub = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / W), first = sub * W;
+  const int tr = (int)threadIdx.x - first * 64;
   const float inv_d = 1.0f / (float)a.D;
   const XT* const x = static_cast<const XT*>(a.x);
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, has_dn = b.dn != nullptr, has_dh = b.dh != nullptr;
@@ -262,8 +268,43 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     for (int j = 0; j < VEC; ++j) acc_pre[c][j] = acc_post[c][j] = acc_gate[c][j] = 0.0f;
     if constexpr (fixed_gate) load_gate<GATE, VEC>(a, 0, min((c * W * 64 + tr) * VEC, a.D - VEC), 1.0f, g[c]);
   }
+  // The norms' weights stay on chip: a row would wait for them once per use (three times 0.7 us).  Up
+  // to 8 elements per lane in registers, else in LDS (one workgroup of 16 waves per CU as it is).
+  constexpr bool IN_LDS = CH * VEC > 8;
+  __shared__ float lds_w[IN_LDS ? 2 * MOE_NORM_MAX_DIM : 1];
+  float w_post[IN_LDS ? 1 : CH][VEC], w_pre[IN_LDS ? 1 : CH][VEC];
+  if constexpr (IN_LDS) {
+    for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
+      lds_w[i] = post ? a.w_post[i] : 1.0f;
+      lds_w[MOE_NORM_MAX_DIM + i] = has_dn ? a.w_pre[i] : 0.0f;
+    }
+    lds_barrier();
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int at = min((c * W * 64 + tr) * VEC, a.D - VEC);
+      if (post) load_row<VEC>(a.w_post + at, w_post[c]);
+      if (has_dn) load_row<VEC>(a.w_pre + at, w_pre[c]);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        w_post[c][j] = post ? w_post[c][j] : 1.0f;
+        w_pre[c][j] = has_dn ? w_pre[c][j] : 0.0f;
+      }
+    }
+  }
+  // weights of the lane's elements of chunk c (columns from `at`)
+  const auto weights = [&](const float (&reg)[IN_LDS ? 1 : CH][VEC], int c, int at, int which, float (&w)[VEC]) {
+    if constexpr (IN_LDS) {
+      load_row<VEC>(lds_w + which * MOE_NORM_MAX_DIM + at, w);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = reg[c][j];
+    }
+  };
   int parity = 0;
-  for (int64_t row = (int64_t)blockIdx.x * R + sub; row < a.T; row += (int64_t)gridDim.x * R, parity ^= 1) {
+  for (int64_t top = (int64_t)blockIdx.x * R; top < a.T; top += (int64_t)gridDim.x * R, parity ^= 1) {
+    const bool live = top + sub < a.T;                        // else a turn without a row: zeros, no stores
+    const int64_t row = live ? top + sub : a.T - 1;
     const int64_t base = row * a.D;
     // opaque, so that the compiler keeps one 32-bit offset instead of a 64-bit address per array and chunk
     int lane_at = tr * VEC;
@@ -285,7 +326,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const bool out = c * W * 64 * VEC + lane_at >= a.D;
+      const bool out = c * W * 64 * VEC + lane_at >= a.D || !live;
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         h[c][j] = out ? 0.0f : h[c][j];
@@ -300,13 +341,13 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
       const int at = min(c * W * 64 * VEC + lane_at, a.D - VEC);
       if (has_y) {
         float w[VEC];
-        if (post) load_row<VEC>(el(a.w_post, at), w);
+        weights(w_post, c, at, 0, w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[c][j] += a.scale * g[c][j] * (post ? y[c][j] * w[j] : y[c][j]);
+        for (int j = 0; j < VEC; ++j) h[c][j] += a.scale * g[c][j] * (y[c][j] * w[j]);
       }
       if (has_dn) {
         float v[VEC];
-        load_row<VEC>(el(a.w_pre, at), v);
+        weights(w_pre, c, at, 1, v);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
           h[c][j] *= rh;                                      // hh
@@ -317,7 +358,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
       }
     }
     if (has_dn) {
-      row_sums<1>(s1, red[parity][0], W);
+      row_sums<1>(s1, red[parity][0], W, first);
       const float m = s1[0] * inv_d;
 #pragma unroll
       for (int c = 0; c < CH; ++c)
@@ -327,7 +368,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = c * W * 64 * VEC + lane_at;
-      if (col < a.D) store_row<VEC>(el(static_cast<XT*>(b.dx) + base, col), e[c]);
+      if (live && col < a.D) store_row<VEC>(el(static_cast<XT*>(b.dx) + base, col), e[c]);
     }
     if (!has_y) continue;
     float s2[2] = {0.0f, 0.0f};
@@ -335,51 +376,79 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     for (int c = 0; c < CH; ++c) {
       const int col = c * W * 64 * VEC + lane_at;
       float w[VEC], dg[VEC];
-      if (post) load_row<VEC>(el(a.w_post, min(col, a.D - VEC)), w);
+      weights(w_post, c, min(col, a.D - VEC), 0, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float se = a.scale * e[c][j];
         const float dz = se * g[c][j];
-        u[c][j] = post ? dz * w[j] : dz;
+        u[c][j] = dz * w[j];
         acc_post[c][j] += dz * y[c][j];
         s2[0] += u[c][j] * y[c][j];
         if constexpr (GATE != MOE_GATE_NONE) {
-          dg[j] = se * (post ? y[c][j] * w[j] : y[c][j]);
+          dg[j] = se * (y[c][j] * w[j]);
           if (sigmoid) dg[j] *= g[c][j] * (1.0f - g[c][j]);
           if constexpr (GATE == MOE_GATE_CHANNEL) acc_gate[c][j] += dg[j];
           if constexpr (GATE == MOE_GATE_TOKEN) s2[1] += dg[j];
         }
       }
       if constexpr (GATE == MOE_GATE_ELEMENT)
-        if (col < a.D) store_row<VEC>(el(static_cast<uint16_t*>(b.dgate) + base, col), dg);
+        if (live && col < a.D) store_row<VEC>(el(static_cast<uint16_t*>(b.dgate) + base, col), dg);
     }
     if constexpr (GATE == MOE_GATE_TOKEN) {
-      row_sums<2>(s2, red[parity][1], W);
-      if (tr == 0) static_cast<float*>(b.dgate)[row] = s2[1];
+      row_sums<2>(s2, red[parity][1], W, first);
+      if (live && tr == 0) static_cast<float*>(b.dgate)[row] = s2[1];
     } else if (post) {
-      row_sums<1>(reinterpret_cast<float(&)[1]>(s2), red[parity][1], W);
+      row_sums<1>(reinterpret_cast<float(&)[1]>(s2), red[parity][1], W, first);
     }
     const float m = post ? s2[0] * inv_d : 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = c * W * 64 * VEC + lane_at;
-      if (col < a.D) {
+      if (live && col < a.D) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[c][j] = ry * (u[c][j] - y[c][j] * m);
         store_row<VEC>(el(b.dy + base, col), u[c]);
       }
     }
   }
-  float* const part = b.part + ((int64_t)blockIdx.x * R + sub) * 3 * a.D;
+  // the rows' sums of the workgroup, added in order into the first row's waves (R > 1: rows of up to
+  // 16 / R waves, so the others' sums of one kind fit SPREAD floats)
+  constexpr int SPREAD = CH * VEC > 8 ? 1 : 64 * MAX_W * CH * VEC;
+  __shared__ float spread[SPREAD];
+  float* const part = b.part + (int64_t)blockIdx.x * 3 * a.D;
+  const auto finish = [&](float (&acc)[CH][VEC], float* out) {
+    const int width = W * 64 * CH * VEC;
+    if constexpr (SPREAD > 1) {
+      if (R > 1) {
+        lds_barrier();                                        // the previous kind has been read
+        if (sub > 0) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int col = (c * W * 64 + tr) * VEC;
-    if (col < a.D) {
-      if (b.dw_pre) store_row<VEC>(part + col, acc_pre[c]);
-      if (b.dw_post) store_row<VEC>(part + a.D + col, acc_post[c]);
-      if constexpr (GATE == MOE_GATE_CHANNEL) store_row<VEC>(part + 2 * (int64_t)a.D + col, acc_gate[c]);
+          for (int c = 0; c < CH; ++c) store_row<VEC>(spread + (sub - 1) * width + (c * W * 64 + tr) * VEC, acc[c]);
+        }
+        lds_barrier();
+        if (sub == 0) {
+          for (int r = 0; r + 1 < R; ++r)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+              float v[VEC];
+              load_row<VEC>(spread + r * width + (c * W * 64 + tr) * VEC, v);
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) acc[c][j] += v[j];
+            }
+        }
+      }
     }
-  }
+    if (sub == 0) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = (c * W * 64 + tr) * VEC;
+        if (col < a.D) store_row<VEC>(out + col, acc[c]);
+      }
+    }
+  };
+  if (b.dw_pre) finish(acc_pre, part);
+  if (b.dw_post) finish(acc_post, part + a.D);
+  if constexpr (GATE == MOE_GATE_CHANNEL) finish(acc_gate, part + 2 * (int64_t)a.D);
 }
 
 // out_k[col] = sum over the partial rows, for the sums that are asked for (blockIdx.y = k).
@@ -411,8 +480,10 @@ Shape norm_shape(int D, int vec) {
   Shape s;
   s.vec = vec;
   const int per_wave = 64 * vec;
-  const int few = vec == 8 ? 1 : 4;
-  s.ch = D <= few * MAX_W * per_wave ? few : vec == 8 ? 2 : vec == 2 ? 8 : 16;
+  const int most = MAX_W * per_wave;                          // elements of one chunk
+  if (vec == 8) s.ch = D <= most ? 1 : 2;
+  else if (vec == 2) s.ch = D <= 2 * most ? 2 : D <= 4 * most ? 4 : 8;
+  else s.ch = D <= 4 * most ? 4 : 16;
   s.W = (D + per_wave * s.ch - 1) / (per_wave * s.ch);
   s.R = s.W == 1 ? 4 : 1;
   s.threads = 64 * s.W * s.R;
@@ -441,7 +512,8 @@ void norm_dispatch(const NormArgs& a, const Shape& sh, const F& f) {
     if (sh.ch == 1) norm_typed<8, 1>(a, f);
     else norm_typed<8, 2>(a, f);
   } else if (sh.vec == 2) {
-    if (sh.ch == 4) norm_typed<2, 4>(a, f);
+    if (sh.ch == 2) norm_typed<2, 2>(a, f);
+    else if (sh.ch == 4) norm_typed<2, 4>(a, f);
     else norm_typed<2, 8>(a, f);
   } else {
     if (sh.ch == 4) norm_typed<1, 4>(a, f);
@@ -472,18 +544,22 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& b, hipStream_t s) 
   const NormArgs& a = b.f;
   const Shape sh = norm_shape(a.D, norm_vec(a.D, {a.x, a.y, a.w_post, wide_gate(a), a.w_pre, b.dh, b.dn, b.dx, b.dy,
                                                   a.gate_kind == MOE_GATE_ELEMENT ? b.dgate : nullptr, b.part}));
-  const int groups = (a.T + sh.R - 1) / sh.R, most = MOE_NORM_PARTS / sh.R;
-  const unsigned grid = (unsigned)(groups < most ? groups : most);
+  // Beyond a row per workgroup, as many rows at a time as 16 waves take: fewer partial sums than
+  // with more workgroups of fewer waves (4096 x 3584: 54 us, 60 with 512 workgroups; 9000 x 130: 14, 17)
+  const int want = (a.T + MOE_NORM_PARTS - 1) / MOE_NORM_PARTS, fit = sh.ch * sh.vec > 8 ? 1 : MAX_W / sh.W;
+  const int R = want < fit ? want : fit;
+  const int groups = R > 0 ? (a.T + R - 1) / R : 0;
+  const unsigned grid = (unsigned)(groups < MOE_NORM_PARTS ? groups : MOE_NORM_PARTS);
   if (grid > 0) {                                             // no rows: the sums below are zero
     norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto xt) {
-      norm_backward_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, sh.threads, 0, s>>>(b, sh.W);
+      norm_backward_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, 64 * sh.W * R, 0, s>>>(b, sh.W, R);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   float* const dgate = a.gate_kind == MOE_GATE_CHANNEL ? static_cast<float*>(b.dgate) : nullptr;
   if (!b.dw_pre && !b.dw_post && !dgate) return hipSuccess;
-  norm_sum_parts_kernel<<<dim3((unsigned)((a.D + 63) / 64), 3), 1024, 0, s>>>(b.part, (int)grid * sh.R, a.D, b.dw_pre,
+  norm_sum_parts_kernel<<<dim3((unsigned)((a.D + 63) / 64), 3), 1024, 0, s>>>(b.part, (int)grid, a.D, b.dw_pre,
                                                                              b.dw_post, dgate);
   return hipGetLastError();
 }
