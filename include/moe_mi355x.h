@@ -438,8 +438,7 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
 /* Most experts and most chosen experts of moe_router. */
 #define MOE_ROUTER_MAX_EXPERTS MOE_SORT_MAX_EXPERTS
 #define MOE_ROUTER_MAX_TOPK 32
-/* Waves per workgroup and most partial sums of the balance statistics. */
-#define MOE_ROUTER_WAVES 16
+/* Most partial sums of the balance statistics. */
 #define MOE_ROUTER_PARTS 256
 
 typedef struct {

@@ -59,25 +59,23 @@ __device__ __forceinline__ float unordered(uint32_t k) {
 template <int VEC>
 __device__ __forceinline__ int column(int i, int lane) { return ((i / VEC) * 64 + lane) * VEC + i % VEC; }
 
-// A row's logits, masked ones (and columns past E) as -inf.
+// -inf for a masked logit (-inf or NaN: fmaxf returns its other operand), at most `top` otherwise.
+__device__ __forceinline__ float sane(float v, float top = BIG) { return __builtin_fminf(__builtin_fmaxf(v, -INFINITY), top); }
+
+// A row's logits; columns past E hold -inf.
 template <class LT, int VEC, int NREG>
 __device__ __forceinline__ void load_logits(const LT* row, int E, int lane, float (&l)[NREG]) {
 #pragma unroll
   for (int c = 0; c < NREG / VEC; ++c) {
-    float v[VEC];
     const int col = (c * 64 + lane) * VEC;
-    if (col < E) {                                            // E % VEC == 0
-      load_row<VEC>(row + col, v);
+    float v[VEC];
+    load_row<VEC>(row + min(col, E - VEC), v);                // E % VEC == 0; lanes past the row read its end
+    const float top = col < E ? BIG : -INFINITY;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) l[c * VEC + j] = v[j] > -INFINITY ? __builtin_fminf(v[j], BIG) : -INFINITY;
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) l[c * VEC + j] = -INFINITY;
-    }
+    for (int j = 0; j < VEC; ++j) l[c * VEC + j] = sane(v[j], top);
   }
 }
 
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, WAVE);
@@ -93,74 +91,123 @@ __device__ __forceinline__ double readlane_d(double v, int l) {
 // The selection key in 64 bits.  m, zd: the row's largest logit and sum of exp(l - m) (softmax).
 __device__ __forceinline__ double exact_key(float l, float bias, int score, float m, double zd) {
   const double x = (double)l;
-  const double s = score == MOE_SCORE_SOFTMAX ? exp(x - (double)m) / zd
-                   : x >= 0.0 ? 1.0 / (1.0 + exp(-x)) : exp(x) / (1.0 + exp(x));
+  const double e = exp(score == MOE_SCORE_SOFTMAX ? x - (double)m : x < 0.0 ? x : -x);
+  const double s = score == MOE_SCORE_SOFTMAX ? e / zd : (x < 0.0 ? e : 1.0) / (1.0 + e);
   return s + (double)bias;
 }
 
-// One wave's row: on return lane r < *chosen holds the expert of rank r (ascending rank), its
-// logit, and -1 / -inf from there on.  cand: CAND entries of this wave.
-template <int VEC, int NREG, bool BIAS>
-__device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias, int E, int K, int score, float m,
-                                       float z, uint2* cand, int lane, int& id, float& logit) {
+// The rare paths read the row again, in loops that are not unrolled: they take no registers from the
+// ordinary one.
+// The sum of exp(l - m) in 64 bits.
+template <class LT>
+__device__ __forceinline__ double exact_sum(const LT* row, int E, float m, int lane) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 64) {
+    float v[1];
+    load_row<1>(row + e, v);
+    const float l = sane(v[0]);
+    if (l > -INFINITY) s += exp((double)l - (double)m);
+  }
+  return wave_sum_f64(s);
+}
+// K maxima over the wave, each over every key that is left.
+template <class LT, bool BIAS>
+__device__ __forceinline__ void choose_in_rounds(const LT* row, const float* bias, int E, int K, int score, float m,
+                                                 int lane, int& id, float& logit) {
+  double zd = 1.0;
+  if (BIAS && score == MOE_SCORE_SOFTMAX) zd = exact_sum(row, E, m, lane);
+  uint32_t taken = 0;                                         // E <= 64 * 32
+#pragma unroll 1
+  for (int r = 0; r < K; ++r) {
+    double wk = -INFINITY;
+    int wc = 0x7FFFFFFF;
+    float wl = -INFINITY;
+#pragma unroll 1
+    for (int i = 0, e = lane; e < E; e += 64, ++i) {
+      float v[1];
+      load_row<1>(row + e, v);
+      const float l = sane(v[0]);
+      if (!(l > -INFINITY) || ((taken >> i) & 1)) continue;
+      double k = (double)l;
+      if constexpr (BIAS) {
+        if (!(bias[e] > -INFINITY)) continue;
+        k = exact_key(l, __builtin_fminf(bias[e], BIG), score, m, zd);
+      }
+      if (wc == 0x7FFFFFFF || k > wk) { wk = k; wc = e; wl = l; }
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) {
+      const double ok = __shfl_xor(wk, d, WAVE);
+      const int oc = __shfl_xor(wc, d, WAVE);
+      const float ol = __shfl_xor(wl, d, WAVE);
+      if (oc != 0x7FFFFFFF && (wc == 0x7FFFFFFF || ok > wk || (ok == wk && oc < wc))) { wk = ok; wc = oc; wl = ol; }
+    }
+    if (wc == 0x7FFFFFFF) break;                              // the same in every lane
+    if ((wc & 63) == lane) taken |= 1u << (wc >> 6);
+    if (lane == r) { id = wc; logit = wl; }
+  }
+}
+
+// One wave's row: on return lane r < K holds the expert of rank r (ascending rank) and its logit, or
+// -1 / -inf where none is left.  cand: CAND entries of this wave.  best: the lane's largest logit.
+template <class LT, int VEC, int NREG, bool BIAS>
+__device__ __forceinline__ void choose(const LT* row, const float (&l)[NREG], float best, const float* bias, int E, int K, int score,
+                                       float m, float z, uint2* cand, int lane, int& id, float& logit) {
   id = -1;
   logit = -INFINITY;
-  uint32_t key[NREG];
-  uint32_t best = 0;
+  float keys[BIAS ? NREG : 1];
+  if constexpr (BIAS) {
+    best = -INFINITY;
+    const float inv_z = 1.0f / z;
 #pragma unroll
-  for (int i = 0; i < NREG; ++i) {
-    if constexpr (BIAS) {
-      const int col = column<VEC>(i, lane);
-      const float b = col < E ? bias[col] : 0.0f;
-      const float s = score == MOE_SCORE_SOFTMAX ? exp_f(l[i] - m) / z : fast_sigmoid(l[i]);
-      key[i] = l[i] > -INFINITY && b > -INFINITY ? ordered(s + __builtin_fminf(b, BIG)) : 0u;
-    } else {
-      key[i] = l[i] > -INFINITY ? ordered(l[i]) : 0u;
+    for (int c = 0; c < NREG / VEC; ++c) {
+      float b[VEC];
+      load_row<VEC>(bias + min((c * 64 + lane) * VEC, E - VEC), b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int i = c * VEC + j;
+        const float s = score == MOE_SCORE_SOFTMAX ? exp_f(l[i] - m) * inv_z : fast_sigmoid(l[i]);
+        keys[i] = l[i] > -INFINITY && b[j] > -INFINITY ? s + __builtin_fminf(b[j], BIG) : -INFINITY;
+        best = __builtin_fmaxf(best, keys[i]);
+      }
     }
-    best = max(best, key[i]);
   }
-  // a bound that at least K lane maxima reach (0 if fewer than K lanes have one)
-  uint32_t bound = 0;
+  const auto key = [&](int i) { return BIAS ? keys[i] : l[i]; };
+  // A bound that at least K lane maxima reach, or the lowest number if fewer lanes have one: found
+  // from the top bit of the ordered keys down, until few enough reach it.
+  const uint32_t ob = best > -INFINITY ? ordered(best) : 0u;
+  uint32_t t = 0;
   for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = bound | (1u << bit);
-    const int n = __popcll(__ballot(best >= t));
+    const uint32_t up = t | (1u << bit);
+    const int n = __popcll(__ballot(ob >= up));
     if (n >= K) {
-      bound = t;
-      if (n <= K + 2) break;
+      t = up;
+      if (n <= K + 3) break;
     }
   }
+  float bound = t ? unordered(t) : -BIG;
   float margin = 0.0f;
   if constexpr (BIAS) {
     // The fp32 keys are off by less than margin / 2: a score by 4e-6 at most (the rounding of the
     // exponents, of the sum of up to 2048 exponentials and of the quotient), the sum of score and
     // bias by 2^-24 of itself.  So every expert among the K largest exact keys has an fp32 key of
     // at least bound - margin.
-    const float b = bound ? unordered(bound) : 0.0f;
-    margin = 1e-5f * (1.0f + __builtin_fabsf(b));
-    if (bound) bound = max(ordered(__builtin_fmaxf(b - margin, -BIG)), 1u);
+    margin = 1e-5f * (1.0f + __builtin_fabsf(bound));
+    bound = __builtin_fmaxf(bound - margin, -BIG);
   }
-  bound = max(bound, 1u);
   int n = 0;
 #pragma unroll
   for (int i = 0; i < NREG; ++i) {
-    const uint64_t mask = __ballot(key[i] >= bound);
+    const bool in = key(i) >= bound;
+    const uint64_t mask = __ballot(in);
     if (mask) {
-      if (key[i] >= bound) {
-        const int p = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
-        if (p < CAND) cand[p] = uint2{__float_as_uint(l[i]), (uint32_t)column<VEC>(i, lane)};
-      }
+      const int p = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+      if (in && p < CAND) cand[p] = uint2{__float_as_uint(l[i]), (uint32_t)column<VEC>(i, lane)};
       n += __popcll(mask);
     }
   }
   wave_sync();
-  double zd = 1.0;
-  const auto exact_z = [&]() {
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < NREG; ++i)
-      if (l[i] > -INFINITY) s += exp((double)l[i] - (double)m);
-    zd = wave_sum_f64(s);
-  };
   if (n <= CAND) {
     const bool have = lane < n;
     const uint2 c = have ? cand[lane] : uint2{0xFF800000u, 0x7FFFFFFFu};
@@ -168,7 +215,7 @@ __device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias
     int rank = 0;
     if constexpr (BIAS) {
       const float b = have ? __builtin_fminf(bias[c.y], BIG) : 0.0f;
-      double k = 0.0;
+      double k = 0.0, zd = 1.0;
       bool done = false;
       if (score == MOE_SCORE_SOFTMAX) {
         // fp32 keys decide unless two of them are close: the sum in 64 bits costs more than the rest
@@ -180,7 +227,7 @@ __device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias
           close |= j != lane && __builtin_fabsf(o - k32) <= 1e-5f * (1.0f + __builtin_fabsf(k32));
         }
         done = __ballot(have && close) == 0;
-        if (!done) exact_z();
+        if (!done) zd = exact_sum(row, E, m, lane);
       }
       if (!done) {
         rank = 0;
@@ -191,12 +238,16 @@ __device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias
           rank += o > k || (o == k && oc < (int)c.y);
         }
       }
+    } else if constexpr (sizeof(LT) == 2) {
+      // bf16: the upper half of the ordered key says it all, the column goes below it
+      const uint32_t k = (ordered(cl) & 0xFFFF0000u) | (0xFFFFu - (c.y & 0xFFFFu));
+      for (int j = 0; j < n; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)k, j) > k;
     } else {
-      const uint32_t k = ordered(cl);
+      const uint64_t k = ((uint64_t)ordered(cl) << 32) | (0xFFFFFFFFu - c.y);
       for (int j = 0; j < n; ++j) {
-        const uint32_t o = __builtin_amdgcn_readlane(k, j);
-        const int oc = __builtin_amdgcn_readlane((int)c.y, j);
-        rank += o > k || (o == k && oc < (int)c.y);
+        const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), j) << 32) |
+                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
+        rank += o > k;
       }
     }
     // to the lane of its rank (ranks of the candidates are 0 .. n - 1, each once)
@@ -211,39 +262,7 @@ __device__ __forceinline__ void choose(const float (&l)[NREG], const float* bias
     wave_sync();
     return;
   }
-  // more than 64 candidates: K maxima, each over every key that is left
-  if constexpr (BIAS)
-    if (score == MOE_SCORE_SOFTMAX) exact_z();
-  uint32_t taken = 0;
-  for (int r = 0; r < K; ++r) {
-    double bk = -INFINITY;
-    int bc = 0x7FFFFFFF, bi = -1;
-    float bl = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NREG; ++i) {
-      if (key[i] >= bound && !((taken >> i) & 1)) {
-        const int col = column<VEC>(i, lane);
-        double k;
-        if constexpr (BIAS) k = exact_key(l[i], __builtin_fminf(bias[col], BIG), score, m, zd);
-        else k = (double)l[i];
-        if (bi < 0 || k > bk) { bk = k; bc = col; bi = i; bl = l[i]; }   // columns ascend with i
-      }
-    }
-    double wk = bk;
-    int wc = bc;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-      const double ok = __shfl_xor(wk, d, WAVE);
-      const int oc = __shfl_xor(wc, d, WAVE);
-      if (ok > wk || (ok == wk && oc < wc)) { wk = ok; wc = oc; }
-    }
-    const bool mine = bi >= 0 && bc == wc;                    // columns are distinct: one lane
-    if (mine) taken |= 1u << bi;
-    const uint64_t who = __ballot(mine);
-    if (!who) break;
-    const float wl = readlane_f(bl, __ffsll((unsigned long long)who) - 1);
-    if (lane == r) { id = wc; logit = wl; }
-  }
+  choose_in_rounds<LT, BIAS>(row, bias, E, K, score, m, lane, id, logit);   // more than 64 candidates
 }
 
 // ws of the balance statistics: [256] a ticket, [parts] Tv, [parts] z sums, [ceil(E / 64)] loss
@@ -269,8 +288,12 @@ __host__ __device__ inline BalanceParts balance_parts(void* ws, int E) {
 }
 
 // Rows wave, wave + waves of the grid, ...
+// Waves of a workgroup: with the balance statistics as many as their registers allow.
+template <int NREG, bool BIAS, bool BAL>
+constexpr int router_waves() { return !BAL ? 4 : BIAS || NREG > 16 ? 8 : 16; }
+
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
-__global__ __launch_bounds__(BAL ? MOE_ROUTER_WAVES * 64 : 256) void router_kernel(const RouterArgs a, void* ws) {
+__global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router_kernel(const RouterArgs a, void* ws) {
   extern __shared__ uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   uint2* const cand = reinterpret_cast<uint2*>(lds) + wave * CAND;
@@ -291,11 +314,12 @@ __global__ __launch_bounds__(BAL ? MOE_ROUTER_WAVES * 64 : 256) void router_kern
     float w = 0.0f;
     if (!a.valid || a.valid[t]) {
       float l[NREG];
-      load_logits<LT, VEC, NREG>(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane, l);
-      float m = -INFINITY;
+      const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
+      load_logits<LT, VEC, NREG>(row, a.E, lane, l);
+      float best = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < NREG; ++i) m = __builtin_fmaxf(m, l[i]);
-      m = wave_max(m);
+      for (int i = 0; i < NREG; ++i) best = __builtin_fmaxf(best, l[i]);
+      const float m = wave_max(best);
       if (m > -INFINITY) {
         float z = 1.0f;
         if (BAL || (a.score == MOE_SCORE_SOFTMAX && (BIAS || !a.renorm))) {
@@ -323,7 +347,7 @@ __global__ __launch_bounds__(BAL ? MOE_ROUTER_WAVES * 64 : 256) void router_kern
           }
         }
         float logit;
-        choose<VEC, NREG, BIAS>(l, a.bias, a.E, a.K, a.score, m, z, cand, lane, id, logit);
+        choose<LT, VEC, NREG, BIAS>(row, l, best, a.bias, a.E, a.K, a.score, m, z, cand, lane, id, logit);
         // with renorm relative to the largest chosen logit: the sum is at least half of that one's term
         float top = a.score == MOE_SCORE_SOFTMAX ? m : 0.0f;
         if (a.renorm) top = __builtin_fminf(wave_max(logit), top);
@@ -397,11 +421,14 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const RouterArgs a
   const int e = blockIdx.x * 64 + lane;
   float p = 0.0f;
   int c = 0;
-  if (e < a.E)
+  {
+    const int at = min(e, a.E - 1);
+#pragma unroll 8
     for (int i = rc; i < parts; i += 16) {
-      p += b.psum[(int64_t)i * a.E + e];
-      c += b.counts[(int64_t)i * a.E + e];
+      p += b.psum[(int64_t)i * a.E + at];
+      c += b.counts[(int64_t)i * a.E + at];
     }
+  }
   ps[rc][lane] = p;
   cs[rc][lane] = c;
   if (rc == 0) {
@@ -483,9 +510,22 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
 #pragma unroll
       for (int i = 0; i < NREG; ++i) l[i] = 0.0f;
     } else {
+      // softmax: ex = exp(l - m); sigmoid: ex = the sigmoid times e^-top, l stays
+      const float top = __builtin_fminf(m, 0.0f);
+      float ex[NREG];
       float z = 1.0f, inv_z = 1.0f;
-      const bool need_p = (softmax && (o.counts || !a.renorm)) || dz != 0.0f;
-      if (need_p) {
+      if (softmax) {
+        if (o.counts || !a.renorm) {
+          z = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) { ex[i] = exp_f(l[i] - m); z += ex[i]; }
+          z = wave_sum(z);
+          inv_z = 1.0f / z;
+        } else {
+#pragma unroll
+          for (int i = 0; i < NREG; ++i) ex[i] = 0.0f;
+        }
+      } else if (dz != 0.0f) {
         z = 0.0f;
 #pragma unroll
         for (int i = 0; i < NREG; ++i) z += exp_f(l[i] - m);
@@ -504,7 +544,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
         if (id >= 0) {
           float one[1];
           load_row<1>(row + id, one);
-          lk = one[0] > -INFINITY ? __builtin_fminf(one[0], BIG) : -INFINITY;
+          lk = sane(one[0]);
           g = a.scale * dw[t * a.K + lane];
           v = softmax ? exp_f(lk - m) * inv_z : fast_sigmoid(lk);
         }
@@ -531,26 +571,21 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
         float mean = 0.0f;
         if (o.counts) {
 #pragma unroll
-          for (int i = 0; i < NREG; ++i) mean += f[i] * exp_f(l[i] - m);
+          for (int i = 0; i < NREG; ++i) mean += f[i] * ex[i];
           mean = wave_sum(mean) * inv_z;
         }
         const float base = mean + tsum;
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) {
-          const int col = column<VEC>(i, lane);
-          const float ex = need_p ? exp_f(l[i] - m) : 0.0f;
-          l[i] = ex * (inv_z * (f[i] - base) + kz) + (dw && col < a.E ? t_row[col] : 0.0f);
-        }
+        for (int i = 0; i < NREG; ++i) l[i] = ex[i] * (inv_z * (f[i] - base) + kz);
       } else {
-        const float top = __builtin_fminf(m, 0.0f);
         float s = 1.0f, mean = 0.0f;
         if (o.counts) {
           s = 0.0f;
 #pragma unroll
           for (int i = 0; i < NREG; ++i) {
-            const float si = sigmoid_over(l[i], top);
-            s += si;
-            mean += f[i] * si;
+            ex[i] = sigmoid_over(l[i], top);
+            s += ex[i];
+            mean += f[i] * ex[i];
           }
           s = wave_sum(s);
           mean = wave_sum(mean);
@@ -559,11 +594,19 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
         mean *= inv_s;
 #pragma unroll
         for (int i = 0; i < NREG; ++i) {
-          const int col = column<VEC>(i, lane);
-          float d = dw && col < a.E ? t_row[col] : 0.0f;
-          if (o.counts) d += sigmoid_over(l[i], top) * (1.0f - fast_sigmoid(l[i])) * (f[i] - mean) * inv_s;
+          float d = 0.0f;
+          if (o.counts) d = ex[i] * (1.0f - fast_sigmoid(l[i])) * (f[i] - mean) * inv_s;
           if (kz != 0.0f) d += kz * exp_f(l[i] - m);
           l[i] = d;
+        }
+      }
+      if (dw) {
+#pragma unroll
+        for (int c = 0; c < NREG / VEC; ++c) {
+          float v[VEC];
+          load_row<VEC>(t_row + min((c * 64 + lane) * VEC, a.E - VEC), v);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) l[c * VEC + j] += v[j];
         }
       }
       if (dw) {
@@ -592,31 +635,32 @@ bool wide_rows(int E, const void* p, const void* q) {
   return E > 256 && E % 8 == 0 && !(((uintptr_t)p | (uintptr_t)q) & 15);
 }
 
+template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
+int forward_rows(const RouterArgs& a, void* ws, hipStream_t s) {
+  constexpr int waves = router_waves<NREG, BIAS, BAL>();
+  int grid = (a.T + waves - 1) / waves;
+  if (BAL) grid = grid < 1 ? 1 : grid < MOE_ROUTER_PARTS ? grid : MOE_ROUTER_PARTS;
+  const size_t lds = waves * CAND * sizeof(uint2) + (BAL ? (size_t)(1 + HAND) * a.E * 4 + 256 : 0);
+  router_kernel<LT, VEC, NREG, BIAS, BAL><<<(unsigned)grid, waves * 64, lds, s>>>(a, ws);
+  return grid;
+}
+// Returns the number of partial sums of the balance statistics.
 template <class LT, int VEC, int NREG>
-void forward_rows(const RouterArgs& a, bool bal, int parts, void* ws, hipStream_t s) {
-  if (bal) {
-    constexpr int waves = MOE_ROUTER_WAVES;
-    const size_t lds = waves * CAND * sizeof(uint2) + (size_t)(1 + HAND) * a.E * 4 + 256;
-    if (a.bias) router_kernel<LT, VEC, NREG, true, true><<<parts, waves * 64, lds, s>>>(a, ws);
-    else router_kernel<LT, VEC, NREG, false, true><<<parts, waves * 64, lds, s>>>(a, ws);
-  } else {
-    constexpr int waves = 4;
-    const unsigned grid = (unsigned)((a.T + waves - 1) / waves);
-    if (a.bias) router_kernel<LT, VEC, NREG, true, false><<<grid, waves * 64, waves * CAND * sizeof(uint2), s>>>(a, nullptr);
-    else router_kernel<LT, VEC, NREG, false, false><<<grid, waves * 64, waves * CAND * sizeof(uint2), s>>>(a, nullptr);
-  }
+int forward_rows(const RouterArgs& a, bool bal, void* ws, hipStream_t s) {
+  if (bal) return a.bias ? forward_rows<LT, VEC, NREG, true, true>(a, ws, s) : forward_rows<LT, VEC, NREG, false, true>(a, ws, s);
+  return a.bias ? forward_rows<LT, VEC, NREG, true, false>(a, ws, s) : forward_rows<LT, VEC, NREG, false, false>(a, ws, s);
 }
 
 template <class LT>
-void forward(const RouterArgs& a, bool bal, int parts, void* ws, hipStream_t s) {
-  if (wide_rows(a.E, a.logits, nullptr)) {
-    if (a.E <= 512) forward_rows<LT, 8, 8>(a, bal, parts, ws, s);
-    else if (a.E <= 1024) forward_rows<LT, 8, 16>(a, bal, parts, ws, s);
-    else forward_rows<LT, 8, 32>(a, bal, parts, ws, s);
+int forward(const RouterArgs& a, bool bal, void* ws, hipStream_t s) {
+  if (wide_rows(a.E, a.logits, a.bias)) {
+    if (a.E <= 512) return forward_rows<LT, 8, 8>(a, bal, ws, s);
+    else if (a.E <= 1024) return forward_rows<LT, 8, 16>(a, bal, ws, s);
+    else return forward_rows<LT, 8, 32>(a, bal, ws, s);
   } else {
-    if (a.E <= 256) forward_rows<LT, 1, 4>(a, bal, parts, ws, s);
-    else if (a.E <= 1024) forward_rows<LT, 1, 16>(a, bal, parts, ws, s);
-    else forward_rows<LT, 1, 32>(a, bal, parts, ws, s);
+    if (a.E <= 256) return forward_rows<LT, 1, 4>(a, bal, ws, s);
+    else if (a.E <= 1024) return forward_rows<LT, 1, 16>(a, bal, ws, s);
+    else return forward_rows<LT, 1, 32>(a, bal, ws, s);
   }
 }
 
@@ -640,10 +684,7 @@ void backward(const RouterArgs& a, const BalanceArgs& o, const float* dw, const 
 }  // namespace
 
 hipError_t launch_router(const RouterArgs& a, const BalanceArgs* b, void* ws, hipStream_t s) {
-  const int groups = (a.T + MOE_ROUTER_WAVES - 1) / MOE_ROUTER_WAVES;
-  const int parts = groups < 1 ? 1 : groups < MOE_ROUTER_PARTS ? groups : MOE_ROUTER_PARTS;
-  if (a.dt == MOE_DT_F32) forward<float>(a, b != nullptr, parts, ws, s);
-  else forward<uint16_t>(a, b != nullptr, parts, ws, s);
+  const int parts = a.dt == MOE_DT_F32 ? forward<float>(a, b != nullptr, ws, s) : forward<uint16_t>(a, b != nullptr, ws, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !b) return e;
   balance_finish_kernel<<<(unsigned)((a.E + 63) / 64), 1024, 0, s>>>(a, *b, ws, parts);
