@@ -23,6 +23,8 @@
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
+#include <type_traits>
+
 namespace moe {
 
 namespace {
@@ -62,19 +64,41 @@ __device__ __forceinline__ int column(int i, int lane) { return ((i / VEC) * 64 
 // -inf for a masked logit (-inf or NaN: fmaxf returns its other operand), at most `top` otherwise.
 __device__ __forceinline__ float sane(float v, float top = BIG) { return __builtin_fminf(__builtin_fmaxf(v, -INFINITY), top); }
 
-// A row's logits; columns past E hold -inf.
+// A row's logits as they are in memory (a row ahead of the one that is worked on), and their values;
+// lanes past the row read its end, and columns past E hold -inf.
 template <class LT, int VEC, int NREG>
-__device__ __forceinline__ void load_logits(const LT* row, int E, int lane, float (&l)[NREG]) {
+struct Row {
+  typedef std::conditional_t<sizeof(LT) == 4, float, uint32_t> word;
+  static constexpr bool PAIRS = sizeof(LT) == 2 && VEC > 1;   // two bf16 per register
+  word raw[PAIRS ? NREG / 2 : NREG];
+  __device__ __forceinline__ void load(const LT* row, int E, int lane) {
 #pragma unroll
-  for (int c = 0; c < NREG / VEC; ++c) {
-    const int col = (c * 64 + lane) * VEC;
-    float v[VEC];
-    load_row<VEC>(row + min(col, E - VEC), v);                // E % VEC == 0; lanes past the row read its end
-    const float top = col < E ? BIG : -INFINITY;
+    for (int c = 0; c < NREG / VEC; ++c) {
+      const LT* const p = row + min((c * 64 + lane) * VEC, E - VEC);   // E % VEC == 0
+      if constexpr (VEC == 8) {
+        constexpr int n = PAIRS ? 1 : 2;                      // 16-byte loads
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) l[c * VEC + j] = sane(v[j], top);
+        for (int k = 0; k < n; ++k) {
+          typedef word word4 __attribute__((ext_vector_type(4)));
+          const word4 q = reinterpret_cast<const word4*>(p)[k];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) raw[(c * n + k) * 4 + j] = q[j];
+        }
+      } else {
+        raw[c] = (word)*p;
+      }
+    }
   }
-}
+  __device__ __forceinline__ void values(int E, int lane, float (&l)[NREG]) const {
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) {
+      const float top = ((i / VEC) * 64 + lane) * VEC < E ? BIG : -INFINITY;
+      if constexpr (sizeof(LT) == 4) l[i] = sane(raw[i], top);
+      else if constexpr (PAIRS) l[i] = sane(__uint_as_float(i % 2 ? raw[i / 2] & 0xFFFF0000u : raw[i / 2] << 16), top);
+      else l[i] = sane(__uint_as_float(raw[i] << 16), top);
+    }
+  }
+};
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -309,13 +333,18 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
     if (blockIdx.x == 0 && threadIdx.x == 0) *balance_parts(ws, a.E).ticket = 0;
     __syncthreads();
   }
-  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves) {
+  const int64_t step = (int64_t)gridDim.x * waves;
+  int64_t t = (int64_t)blockIdx.x * waves + wave;
+  Row<LT, VEC, NREG> ahead;
+  if (t < a.T) ahead.load(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane);
+  for (; t < a.T; t += step) {
+    const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
     int id = -1;
     float w = 0.0f;
+    float l[NREG];
+    ahead.values(a.E, lane, l);
+    if (BAL && t + step < a.T) ahead.load(row + step * a.E, a.E, lane);
     if (!a.valid || a.valid[t]) {
-      float l[NREG];
-      const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
-      load_logits<LT, VEC, NREG>(row, a.E, lane, l);
       float best = -INFINITY;
 #pragma unroll
       for (int i = 0; i < NREG; ++i) best = __builtin_fmaxf(best, l[i]);
@@ -479,29 +508,41 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
                                                               LT* __restrict__ dlogits) {
   extern __shared__ float spread[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  float* const t_row = spread + wave * a.E;
+  float* const f = spread;                                    // [E] a_i
+  float* const t_row = spread + (1 + wave) * a.E;             // [E] of this wave
   for (int e = lane; e < a.E; e += 64) t_row[e] = 0.0f;
-  wave_sync();
+  const int64_t step = (int64_t)gridDim.x * waves;
+  int64_t t = (int64_t)blockIdx.x * waves + wave;
+  Row<LT, VEC, NREG> ahead;
+  if (t < a.T) ahead.load(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane);
   const int tv = o.counts ? *o.num_valid : 0;
   const bool softmax = a.score == MOE_SCORE_SOFTMAX;
   const float db = o.counts && tv > 0 ? (dloss ? dloss[0] : 1.0f) * o.coef : 0.0f;
   const float dz = o.counts && tv > 0 ? (dloss ? dloss[1] : 1.0f) * o.z_coef * 2.0f / (float)tv : 0.0f;
-  float f[NREG];
   {
     const float k = tv > 0 ? db * (float)a.E / ((float)a.K * (float)tv * (float)tv) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < NREG; ++i) {
-      const int col = column<VEC>(i, lane);
-      f[i] = o.counts && col < a.E ? k * (float)o.counts[col] : 0.0f;
-    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) f[e] = o.counts ? k * (float)o.counts[e] : 0.0f;
   }
-  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves) {
+  __syncthreads();
+  // this lane's a_i of chunk c
+  const auto balance = [&](int c, float (&v)[VEC]) { load_row<VEC>(f + min((c * 64 + lane) * VEC, a.E - VEC), v); };
+  for (; t < a.T; t += step) {
     const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
     LT* const out = dlogits + t * a.E;
+    // the chosen experts' ids, gradients and logits are asked for before anything waits
+    int id = -1;
+    float g = 0.0f, one[1] = {-INFINITY};
+    if (dw && lane < a.K) {
+      id = a.ids[t * a.K + lane];
+      g = a.scale * dw[t * a.K + lane];
+    }
+    if ((unsigned)id >= (unsigned)a.E) id = -1;
+    if (id >= 0) load_row<1>(row + id, one);
     float l[NREG];
+    ahead.values(a.E, lane, l);
+    if (t + step < a.T) ahead.load(row + step * a.E, a.E, lane);
     float m = -INFINITY;
     if (!a.valid || a.valid[t]) {
-      load_logits<LT, VEC, NREG>(row, a.E, lane, l);
 #pragma unroll
       for (int i = 0; i < NREG; ++i) m = __builtin_fmaxf(m, l[i]);
       m = wave_max(m);
@@ -534,20 +575,10 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
       }
       // the chosen experts' part
       float tsum = 0.0f;
-      int id = -1;
       if (dw) {
-        float v = 0.0f, g = 0.0f, lk = -INFINITY;
-        if (lane < a.K) {
-          id = a.ids[t * a.K + lane];
-          if ((unsigned)id >= (unsigned)a.E) id = -1;
-        }
-        if (id >= 0) {
-          float one[1];
-          load_row<1>(row + id, one);
-          lk = sane(one[0]);
-          g = a.scale * dw[t * a.K + lane];
-          v = softmax ? exp_f(lk - m) * inv_z : fast_sigmoid(lk);
-        }
+        const float lk = sane(one[0]);
+        if (id < 0) g = 0.0f;
+        const float v = id < 0 ? 0.0f : softmax ? exp_f(lk - m) * inv_z : fast_sigmoid(lk);
         float tk;
         if (a.renorm) {
           const float top = __builtin_fminf(wave_max(lk), softmax ? m : 0.0f);
@@ -571,21 +602,37 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
         float mean = 0.0f;
         if (o.counts) {
 #pragma unroll
-          for (int i = 0; i < NREG; ++i) mean += f[i] * ex[i];
+          for (int c = 0; c < NREG / VEC; ++c) {
+            float v[VEC];
+            balance(c, v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) mean += v[j] * ex[c * VEC + j];
+          }
           mean = wave_sum(mean) * inv_z;
         }
         const float base = mean + tsum;
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) l[i] = ex[i] * (inv_z * (f[i] - base) + kz);
+        for (int c = 0; c < NREG / VEC; ++c) {
+          float v[VEC];
+          balance(c, v);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) l[c * VEC + j] = ex[c * VEC + j] * (inv_z * (v[j] - base) + kz);
+        }
       } else {
         float s = 1.0f, mean = 0.0f;
         if (o.counts) {
           s = 0.0f;
 #pragma unroll
-          for (int i = 0; i < NREG; ++i) {
-            ex[i] = sigmoid_over(l[i], top);
-            s += ex[i];
-            mean += f[i] * ex[i];
+          for (int c = 0; c < NREG / VEC; ++c) {
+            float v[VEC];
+            balance(c, v);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const int i = c * VEC + j;
+              ex[i] = sigmoid_over(l[i], top);
+              s += ex[i];
+              mean += v[j] * ex[i];
+            }
           }
           s = wave_sum(s);
           mean = wave_sum(mean);
@@ -593,11 +640,17 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
         const float inv_s = 1.0f / s;                         // at least half of one term
         mean *= inv_s;
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) {
-          float d = 0.0f;
-          if (o.counts) d = ex[i] * (1.0f - fast_sigmoid(l[i])) * (f[i] - mean) * inv_s;
-          if (kz != 0.0f) d += kz * exp_f(l[i] - m);
-          l[i] = d;
+        for (int c = 0; c < NREG / VEC; ++c) {
+          float v[VEC];
+          balance(c, v);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const int i = c * VEC + j;
+            float d = 0.0f;
+            if (o.counts) d = ex[i] * (1.0f - fast_sigmoid(l[i])) * (v[j] - mean) * inv_s;
+            if (kz != 0.0f) d += kz * exp_f(l[i] - m);
+            l[i] = d;
+          }
         }
       }
       if (dw) {
@@ -668,7 +721,7 @@ template <class LT>
 void backward(const RouterArgs& a, const BalanceArgs& o, const float* dw, const float* dloss, void* dlogits, hipStream_t s) {
   const unsigned groups = (unsigned)((a.T + 3) / 4);
   const unsigned grid = groups < 1024u ? groups : 1024u;
-  const size_t lds = (size_t)4 * a.E * 4;
+  const size_t lds = (size_t)5 * a.E * 4;
   LT* const d = static_cast<LT*>(dlogits);
   if (wide_rows(a.E, a.logits, dlogits)) {
     if (a.E <= 512) router_backward_kernel<LT, 8, 8><<<grid, 256, lds, s>>>(a, o, dw, dloss, d);
