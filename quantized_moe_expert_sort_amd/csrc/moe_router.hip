@@ -406,33 +406,34 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
       b.z[blockIdx.x] = q;
     }
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) b.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
-    // the waves' sums: at most HAND waves at a time hand theirs to as many lower ones, until one is left
-    for (int left = waves; left > 1;) {
-      const int n = left / 2 < HAND ? left / 2 : HAND;        // waves [left - n, left) hand to [left - 2 n, left - n)
+    // the waves' probability sums, HAND waves at a time through LDS; each thread adds its columns in
+    // the order of the waves
+    constexpr int COLS = (64 * NREG + 64 * router_waves<NREG, BIAS, BAL>() - 1) / (64 * router_waves<NREG, BIAS, BAL>());
+    float sum[COLS] = {};
+    for (int base = 0; base < waves; base += HAND) {
       __syncthreads();
-      if (wave >= left - n && wave < left) {
+      if (wave >= base && wave < base + HAND) {
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) {
-          const int col = column<VEC>(i, lane);
-          if (col < a.E) handed[(wave - left + n) * a.E + col] = psum[i];
+        for (int c = 0; c < NREG / VEC; ++c) {
+          const int col = (c * 64 + lane) * VEC;
+          float v[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) v[j] = psum[c * VEC + j];
+          if (col < a.E) store_row<VEC>(handed + (wave - base) * a.E + col, v);
         }
       }
       __syncthreads();
-      if (wave >= left - 2 * n && wave < left - n) {
 #pragma unroll
-        for (int i = 0; i < NREG; ++i) {
-          const int col = column<VEC>(i, lane);
-          if (col < a.E) psum[i] += handed[(wave - left + 2 * n) * a.E + col];
-        }
+      for (int c = 0; c < COLS; ++c) {
+        const int col = min(c * (int)blockDim.x + (int)threadIdx.x, a.E - 1);
+#pragma unroll
+        for (int k = 0; k < HAND; ++k) sum[c] += handed[k * a.E + col];
       }
-      left -= n;
     }
-    if (wave == 0) {
 #pragma unroll
-      for (int i = 0; i < NREG; ++i) {
-        const int col = column<VEC>(i, lane);
-        if (col < a.E) b.psum[(int64_t)blockIdx.x * a.E + col] = psum[i];
-      }
+    for (int c = 0; c < COLS; ++c) {
+      const int col = c * blockDim.x + threadIdx.x;
+      if (col < a.E) b.psum[(int64_t)blockIdx.x * a.E + col] = sum[c];
     }
   }
 }
