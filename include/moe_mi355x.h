@@ -387,7 +387,7 @@ typedef struct {
   int32_t gate_act;     /* moe_gate_act_t */
   int32_t q_dt;         /* MOE_DT_FP8_E4M3, MOE_DT_FP4_E2M1 or MOE_DT_I8; read only when q is given */
   float scale;          /* of the block's output, finite */
-  float eps;            /* of both norms, finite and > 0 */
+  float eps;            /* of both norms, a normal number > 0 */
 } moe_block_norm_t;
 
 /* moe_block_norm -- the norm after one block, its gate, the residual sum and the norm before the

@@ -294,7 +294,7 @@ moe_status_t check_norm(const moe_block_norm_t* p, moe::NormArgs* a) {
   if (p->gate_kind < MOE_GATE_NONE || p->gate_kind > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
   if (p->gate_act != MOE_GATE_RAW && p->gate_act != MOE_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (p->gate_kind == MOE_GATE_NONE && p->gate_act != MOE_GATE_RAW) return MOE_ERR_INVALID_ARG;
-  if (!std::isfinite(p->scale) || !std::isfinite(p->eps) || p->eps <= 0.f) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(p->scale) || !std::isnormal(p->eps) || p->eps <= 0.f) return MOE_ERR_INVALID_ARG;
   if ((p->gate_kind == MOE_GATE_NONE) != (p->gate == nullptr) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
   if (!p->y && (p->w_post || p->gate_kind != MOE_GATE_NONE) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
   if (p->dim > MOE_NORM_MAX_DIM) return MOE_ERR_UNSUPPORTED;

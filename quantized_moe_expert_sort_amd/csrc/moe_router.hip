@@ -318,7 +318,7 @@ constexpr int router_waves() { return !BAL ? 4 : BIAS || NREG > 16 ? 8 : 16; }
 
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
 __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router_kernel(const RouterArgs a, void* ws) {
-  extern __shared__ uint8_t lds[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   uint2* const cand = reinterpret_cast<uint2*>(lds) + wave * CAND;
   int32_t* const hist = reinterpret_cast<int32_t*>(lds + (size_t)waves * CAND * sizeof(uint2));   // BAL: [E]
@@ -507,7 +507,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
                                                               const float* __restrict__ dw,
                                                               const float* __restrict__ dloss,
                                                               LT* __restrict__ dlogits) {
-  extern __shared__ float spread[];
+  extern __shared__ __attribute__((aligned(16))) float spread[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   float* const f = spread;                                    // [E] a_i
   float* const t_row = spread + (1 + wave) * a.E;             // [E] of this wave

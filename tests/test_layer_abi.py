@@ -75,7 +75,7 @@ def norm_status(**kw):
 def test_block_norm_refusals():
     assert qm.lib().moe_block_norm(None, None) == INVALID
     for bad in (dict(tokens=-1), dict(dim=0), dict(dim=-5), dict(x_dt=1), dict(x_dt=4), dict(gate_kind=4), dict(gate_kind=-1),
-                dict(gate_act=2), dict(gate_act=1), dict(scale=NAN), dict(scale=INF), dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN),
+                dict(gate_act=2), dict(gate_act=1), dict(scale=NAN), dict(scale=INF), dict(eps=0.0), dict(eps=-1.0), dict(eps=NAN), dict(eps=1e-40),
                 dict(gate=P), dict(gate_kind=1), dict(x=None), dict(y=None), dict(y=None, w_post=None, gate=P, gate_kind=2),
                 dict(w_pre=None), dict(h=None, n=None), dict(q=P), dict(q_scale=P), dict(q=P, q_scale=P, q_dt=0),
                 dict(q=P, q_scale=P, q_dt=3), dict(q=P, q_scale=P, q_dt=1, n=None, w_pre=None),
