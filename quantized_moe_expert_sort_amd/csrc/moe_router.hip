@@ -440,7 +440,7 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
 
 // The batch's statistics from the workgroups' partial sums, 64 experts per workgroup: 16 row
 // classes add their partial rows in order, then the classes are added in order.  The workgroup
-// that takes the last ticket adds the workgroups' loss parts, again in order.
+// that takes the last ticket adds the workgroups' loss parts, in the order of a wave's reduction.
 __global__ __launch_bounds__(1024) void balance_finish_kernel(const RouterArgs a, const BalanceArgs o, void* ws, int parts) {
   __shared__ float ps[16][64];
   __shared__ int cs[16][64];
@@ -482,16 +482,18 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const RouterArgs a
     part = (float)c * mean;
   }
   part = wave_sum(part);
-  if (lane != 0) return;
   float total = part;
   if (gridDim.x > 1) {
-    __hip_atomic_store(&b.loss[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const int ticket = __hip_atomic_fetch_add(b.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    if (ticket != (int)gridDim.x - 1) return;
-    total = 0.0f;
-    for (unsigned i = 0; i < gridDim.x; ++i)
-      total += __hip_atomic_load(&b.loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    int ticket = 0;
+    if (lane == 0) {
+      __hip_atomic_store(&b.loss[blockIdx.x], part, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      ticket = __hip_atomic_fetch_add(b.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(ticket) != (int)gridDim.x - 1) return;
+    // at most MOE_ROUTER_MAX_EXPERTS / 64 parts: one per lane, in one round trip
+    total = wave_sum(lane < (int)gridDim.x ? __hip_atomic_load(&b.loss[lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f);
   }
+  if (lane != 0) return;
   o.num_valid[0] = tv;
   o.loss[0] = tv > 0 ? o.coef * total * ((float)a.E / ((float)a.K * (float)tv)) : 0.0f;
   o.loss[1] = tv > 0 && o.z_coef != 0.0f ? o.z_coef * s_z / (float)tv : 0.0f;   // s_z may be infinite
