@@ -14,6 +14,12 @@
 // in bf16 would carry its rounding into the gradients); its sums over rows are kept in registers
 // over the rows a workgroup takes, written as partial sums and added in a fixed order by a second
 // launch, so that the gradients do not depend on timing.
+//
+// Measured on MI355X (a 2 GiB copy runs at 4.9 TB/s): forward 8192 x 3584 bf16 with fp8 codes 51 us
+// (265 MB: 54 us at the copy's rate), 4096 x 3584 with an fp32 stream 37 us (176 MB), one row 3.3 us;
+// backward 4096 x 3584, fp32 stream, gate per channel 48 us and 4.5 for the partial sums (264 MB).
+// Rows of more than 8192 elements with a gate per channel spill in the backward pass (100 x 12000:
+// 41 us, 16 without the gate).
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
