@@ -83,13 +83,15 @@ __device__ __forceinline__ float rsqrt_f(float v) {
   const float e = __builtin_fmaf(-v * r, r, 1.0f);
   return r > 0.0f && r < INFINITY ? __builtin_fmaf(0.5f * r, e, r) : r;
 }
-// sigmoid with the rounding of the exponent's product and of the reciprocal taken back (2 ulp)
+// sigmoid with the rounding of the exponent's product and of the reciprocal taken back (2 ulp); 0 or 1
+// where the exponent leaves the range (infinities too), NaN of NaN
 __device__ __forceinline__ float sigmoid_f(float x) {
   constexpr float L2E = 1.4426950408889634f, L2E_LOW = 1.92596299e-8f;
-  const float t = __builtin_fminf(-L2E * x, 126.0f);
+  const float p = -L2E * x;
+  const float t = p > 126.0f ? 126.0f : p;                    // a comparison: fminf would lose NaN
   const float low = __builtin_fmaf(-L2E, x, -t) - L2E_LOW * x;
   const float e = __builtin_amdgcn_exp2f(t);
-  const float d = 1.0f + (t < 126.0f ? __builtin_fmaf(e, low * 0.6931472f, e) : e);
+  const float d = 1.0f + (t < 126.0f && t > -126.0f ? __builtin_fmaf(e, low * 0.6931472f, e) : e);
   const float r = __builtin_amdgcn_rcpf(d);
   return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }

@@ -154,6 +154,27 @@ def test_rows_with_infinity_or_nan_stay_to_themselves():
     assert torch.isnan(r.q_scale[[1, 3]]).all() and (r.q[[1, 3]] == 0).all()
 
 
+@pytest.mark.parametrize("D", [96, 97])
+def test_gates_far_out(D):
+    # a sigmoid of +-inf and of numbers whose exponent overflows is 1 or 0; NaN stays NaN in its row
+    gate = torch.tensor([float("inf"), -float("inf"), 3e38, -3e38, 100.0, -100.0, 0.0, -0.0, float("nan"), 1.0])
+    T = gate.numel()
+    c = make(T, D, torch.float32)
+    d = gpu(c)
+    kw = dict(w_post=d["w_post"], gate=gate.cuda(), gate_kind="token", gate_act="sigmoid", w_pre=d["w_pre"])
+    r = qm.moe_block_norm(d["x"], d["y"], eps=1e-5, stats=True, **kw)
+    w = {k: ref.f64(v) for k, v in c.items()}
+    h, n, mag = ref.norm_forward(w["x"], w["y"], w["w_post"], gate.double(), "token", "sigmoid", 1.0, w["w_pre"], 1e-5)
+    fine = ~torch.isnan(gate)
+    close(r.h[fine.cuda()], h[fine], mag[fine])
+    assert torch.isnan(r.h[~fine.cuda()]).all() and torch.isnan(r.n[~fine.cuda()]).all()
+    b = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, d["dh"], d["dn"], **kw)
+    want, m = ref.norm_backward(w["x"][fine], w["y"][fine], w["w_post"], gate.double()[fine], "token", "sigmoid", 1.0, w["w_pre"],
+                                1e-5, w["dh"][fine], w["dn"][fine])
+    for k in ("dx", "dy", "dgate"):
+        close(getattr(b, k)[fine.cuda()], want[k], 3 * m[k], 1e-30)
+
+
 @pytest.mark.parametrize("T,D", [(1, 32), (3, 512), (5, 544), (17, 3584), (2, 16384)])
 @pytest.mark.parametrize("kind", ["fp8", "fp4", "i8"])
 def test_codes(T, D, kind):
