@@ -473,7 +473,7 @@ static inline size_t moe_router_ws_bytes(int32_t num_experts) {
  *     topk_w:   scale * s[id], with renorm divided by the sum of the chosen s
  * The choice does not depend on rounding: keys with a bias are compared in 64 bits where fp32
  * could not tell.  A logit of -inf or NaN, or a bias of -inf or NaN, masks its expert; +inf counts
- * as the largest finite value, -0 as 0.  Slots left over (fewer than topk unmasked experts, an invalid
+ * as the largest finite fp32 value, -0 as 0.  Slots left over (fewer than topk unmasked experts, an invalid
  * token) get id -1 and weight 0; moe_sort skips them.
  *   balance   or NULL: statistics of the batch, from the same pass over the logits.  Over the Tv
  *             counted tokens (valid, with an unmasked logit), p = softmax(logits) or s / sum(s):

@@ -266,8 +266,9 @@ __device__ __forceinline__ void choose(const LT* row, const float (&l)[NREG], fl
         }
       }
     } else if constexpr (sizeof(LT) == 2) {
-      // bf16: the upper half of the ordered key says it all, the column goes below it
-      const uint32_t k = (ordered(cl) & 0xFFFF0000u) | (0xFFFFu - (c.y & 0xFFFFu));
+      // bf16: the upper half of the ordered key says it all (rounded up, so that a clamped +inf, the one
+      // value that is no bf16, stays above the largest bf16), the column goes below it
+      const uint32_t k = ((ordered(cl) + 0xFFFFu) & 0xFFFF0000u) | (0xFFFFu - (c.y & 0xFFFFu));
       for (int j = 0; j < n; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)k, j) > k;
     } else {
       const uint64_t k = ((uint64_t)ordered(cl) << 32) | (0xFFFFFFFFu - c.y);
@@ -314,15 +315,15 @@ __host__ __device__ inline BalanceParts balance_parts(void* ws, int E) {
   return b;
 }
 
-// Rows wave, wave + waves of the grid, ...
 // Waves of a workgroup: with the balance statistics as many as their registers allow.
 template <int NREG, bool BIAS, bool BAL>
 constexpr int router_waves() { return !BAL ? 4 : BIAS || NREG > 16 ? 8 : 16; }
 
+// Rows wave, wave + waves of the grid, ...
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
 __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router_kernel(const RouterArgs a, void* ws) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   uint2* const cand = reinterpret_cast<uint2*>(lds) + wave * CAND;
   int32_t* const hist = reinterpret_cast<int32_t*>(lds + (size_t)waves * CAND * sizeof(uint2));   // BAL: [E]
   float* const handed = reinterpret_cast<float*>(hist + a.E);                                     // BAL: [HAND, E]
@@ -513,7 +514,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
                                                               const float* __restrict__ dloss,
                                                               LT* __restrict__ dlogits) {
   extern __shared__ __attribute__((aligned(16))) float spread[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   float* const f = spread;                                    // [E] a_i
   float* const t_row = spread + (1 + wave) * a.E;             // [E] of this wave
   for (int e = lane; e < a.E; e += 64) t_row[e] = 0.0f;

@@ -167,6 +167,18 @@ def test_masked_experts(dt, score, E):
     check(logits, K, score, bias=bias, z_coef=0.0, train=False)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_infinity_comes_before_the_largest_finite_logit(dt):
+    # +inf counts as fp32's largest value, which no bf16 holds: above bf16's largest, level with fp32's
+    logits, _ = make(3, 300, dt)
+    logits[0, 10], logits[0, 200] = torch.finfo(dt).max, math.inf
+    logits[1, 10], logits[1, 200], logits[1, 201] = math.inf, torch.finfo(dt).max, math.inf
+    logits[2, :] = torch.finfo(dt).max
+    logits[2, 299] = math.inf
+    check(logits, 4, z_coef=0.0)
+    check(logits, 4, "sigmoid", z_coef=0.0)
+
+
 def test_no_counted_token():
     logits, _ = make(5, 40)
     r = check(logits, 3, valid=torch.zeros(5, dtype=torch.bool))
