@@ -1,0 +1,81 @@
+"""The operators around the routed experts on tensors of more than 2^31 elements: the last rows have
+to give the bits that the same rows give alone, and the sums over rows those of the rows that are
+not zero."""
+import pytest
+import torch
+
+import quantized_moe_expert_sort_amd as qm
+
+pytestmark = pytest.mark.gpu
+ROWS = 3                                                       # random rows at the end
+
+
+@pytest.fixture(autouse=True)
+def give_memory_back():
+    yield
+    torch.cuda.empty_cache()
+
+
+def tail(T, D, dtype, seed):
+    """(zeros [T, D] with random last rows, those rows alone)"""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    last = torch.randn(ROWS, D, device="cuda", generator=g).to(dtype)
+    full = torch.zeros(T, D, dtype=dtype, device="cuda")
+    full[-ROWS:] = last
+    return full, last
+
+
+def test_block_norm():
+    T, D = 140_000, 15_360                                     # 2.15e9 elements
+    (x, xs), (y, ys), (dh, dhs), (dn, dns) = (tail(T, D, torch.bfloat16, s) for s in range(4))
+    w, v = torch.rand(D, device="cuda") + 0.5, torch.rand(D, device="cuda") + 0.5
+    kw = dict(w_post=w, w_pre=v)
+    big, small = (qm.moe_block_norm(a, b, stats=True, q_dtype="fp8", **kw) for a, b in ((x, y), (xs, ys)))
+    for k in ("h", "n", "q", "q_scale"):
+        assert torch.equal(getattr(big, k)[-ROWS:], getattr(small, k)), k
+    assert torch.equal(big.rstd[:, -ROWS:], small.rstd)
+    assert not big.h[:-ROWS].any() and not big.n[:-ROWS].any()
+    rstd, srstd, n = big.rstd, small.rstd, small.n
+    del big, small
+    a = qm.moe_block_norm_backward(x, y, rstd, dh, dn, **kw)
+    b = qm.moe_block_norm_backward(xs, ys, srstd, dhs, dns, **kw)
+    assert torch.equal(a.dx[-ROWS:], b.dx) and torch.equal(a.dy[-ROWS:], b.dy)
+    # zero rows add nothing; the sums of three terms may be added in another order: two roundings a
+    # side of at most the sum of the terms' magnitudes (taken from bf16 outputs, so 1% more)
+    terms = {"dw_pre": dns.float() * n.float() / v, "dw_post": b.dx.float() * ys.float() * srstd[0][:, None]}
+    for k, t in terms.items():
+        assert ((getattr(a, k) - getattr(b, k)).abs() <= 4 * 2.0 ** -24 * 1.01 * t.abs().sum(0)).all(), k
+
+
+def test_router():
+    T, E, K = 2_100_000, 1032, 2                               # 2.17e9 logits
+    logits, last = tail(T, E, torch.bfloat16, 5)
+    big, small = qm.moe_router(logits, K, balance=(0.1, 0.1)), qm.moe_router(last, K)
+    assert torch.equal(big.ids[-ROWS:], small.ids) and torch.equal(big.w[-ROWS:], small.w)
+    assert (big.ids[:-ROWS] == torch.tensor([0, 1], dtype=torch.int32, device="cuda")).all()
+    assert int(big.balance.num_valid) == T and int(big.balance.counts.sum()) == T * K
+    dw = torch.randn(T, K, device="cuda")
+    a = qm.moe_router_backward(logits, big._replace(balance=None), dw)
+    b = qm.moe_router_backward(last, small, dw[-ROWS:].clone())
+    assert torch.equal(a[-ROWS:], b)
+
+
+@pytest.mark.parametrize("T,N,K", [(2_000_000, 1100, 16), (1_050_000, 16, 4112)])
+def test_product(T, N, K):                                     # 2.2e9 outputs; 4.3e9 bytes of tokens
+    g = torch.Generator(device="cuda").manual_seed(9)
+    last = torch.randint(-127, 128, (ROWS, K), device="cuda", generator=g, dtype=torch.int32).to(torch.int8)
+    a = torch.zeros(T, K, dtype=torch.int8, device="cuda")
+    a[-ROWS:] = last
+    w = qm.moe_pack_i8(torch.randint(-127, 128, (N, K), device="cuda", generator=g, dtype=torch.int32).to(torch.int8))
+    sa, sw = torch.rand(T, device="cuda") + 0.5, torch.rand(N, device="cuda") / K
+    out = qm.moe_gemm_i8(a, sa, w, sw)
+    assert torch.equal(out[-ROWS:], qm.moe_gemm_i8(last, sa[-ROWS:].clone(), w, sw))
+    assert not out[:-ROWS].any()
+
+
+def test_quant():
+    x, last = tail(140_000, 15_360, torch.bfloat16, 11)
+    q, s = qm.moe_quant_i8(x)
+    ql, sl = qm.moe_quant_i8(last)
+    assert torch.equal(q[-ROWS:], ql) and torch.equal(s[-ROWS:], sl)
+    assert not q[:-ROWS].any() and not s[:-ROWS].any()
