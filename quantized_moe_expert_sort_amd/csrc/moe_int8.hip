@@ -26,6 +26,7 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));   // 8 bf16 of a row of any length
 
 // ---------------------------------------------------------------- coding of rows
 
@@ -357,8 +358,10 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
   }
 
   // epilogue: register i of lane l is weight row 8 (i / 4) + 4 (l / 32) + i % 4, token l % 32
+  // Eight channels go out together wherever a row starts (the loads and stores of global memory need
+  // no alignment): 7508 x 866 x 320 with add 14.3 us, 38 with an element at a time; 2000 x 4099 x 512
+  // 25 and 41.  Rows in multiples of 16 bytes take as long as with aligned accesses.
   constexpr int FO = ACT ? FN / 2 : FN;                       // 32-channel groups of outputs
-  const bool wide = p.No % 8 == 0 && !(((uintptr_t)p.out | (uintptr_t)p.add) & 15);
 #pragma unroll
   for (int n = 0; n < FO; ++n) {
     const int cw = c0 + wn * (FO * 32) + n * 32;              // first channel of the group
@@ -373,34 +376,30 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
         v[i] = (float)acc[n][m][i] * (sa * p.sw[c]);
         if constexpr (ACT) v[i] = activate(p, v[i], (float)acc[n + FO][m][i] * (sa * p.sw[p.No + c]));
       }
-      if (wide) {
-        // halves of two 8-channel groups exchanged: lanes 0..31 hold the first, 32..63 the second
+      // halves of two 8-channel groups exchanged: lanes 0..31 hold the first, 32..63 the second
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float w[8];
+      for (int j = 0; j < 2; ++j) {
+        float w[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[8 * j + i]), __float_as_uint(v[8 * j + 4 + i]),
-                                                            false, false);
-            w[i] = __uint_as_float(s[0]);
-            w[4 + i] = __uint_as_float(s[1]);
-          }
-          const int c = cw + 16 * j + 8 * hl;
-          if (t < p.T && c < p.No) {
-            if (p.add) {
-              float o[8];
-              load_row<8>(p.add + t * p.No + c, o);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) w[i] += o[i];
-            }
-            store_row<8>(p.out + t * p.No + c, w);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[8 * j + i]), __float_as_uint(v[8 * j + 4 + i]),
+                                                          false, false);
+          w[i] = __uint_as_float(s[0]);
+          w[4 + i] = __uint_as_float(s[1]);
         }
-      } else {
+        const int c = cw + 16 * j + 8 * hl;
+        if (t < p.T && c + 8 <= p.No) {
+          if (p.add) {
+            const v4u_any q = *reinterpret_cast<const v4u_any*>(p.add + t * p.No + c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int c = cw + 8 * (i / 4) + 4 * hl + i % 4;
-          if (t < p.T && c < p.No) store_one(p, t, c, v[i]);
+            for (int i = 0; i < 8; ++i) w[i] += __uint_as_float(i & 1 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16);
+          }
+          *reinterpret_cast<v4u_any*>(p.out + t * p.No + c) =
+              v4u_any{bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
+        } else if (t < p.T) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < p.No) store_one(p, t, c + i, w[i]);
         }
       }
     }

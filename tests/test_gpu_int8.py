@@ -76,6 +76,22 @@ def test_tile_shapes(T, N, K):
     check(T, N, K, add=K == 272)
 
 
+@pytest.mark.parametrize("N", [96, 129, 258, 1004])
+@pytest.mark.parametrize("off", [0, 1, 2, 5])
+@pytest.mark.parametrize("T", [9, 50, 700])
+def test_rows_at_any_address(T, N, off):
+    # out and add start at any element: neither their start nor their rows are aligned
+    c = make(T, N, 144, add=True)
+    buf = torch.full((T * N + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+    add = torch.empty(T * N + 16, dtype=torch.bfloat16, device="cuda")[off:off + T * N].view(T, N)
+    add.copy_(c["add"])
+    out = buf[8 - off:8 - off + T * N].view(T, N)
+    qm.moe_gemm_i8(c["a"].cuda(), c["sa"].cuda(), qm.moe_pack_i8(c["w"].cuda()), c["sw"].cuda(), add=add, out=out)
+    assert (buf[:8 - off] == 7).all() and (buf[8 - off + T * N:] == 7).all()
+    want, err = ref.gemm_i8(c["a"], c["sa"], c["w"], c["sw"], add=c["add"])
+    assert not ((ref.f64(out) - want).abs() > ref.HALF_BF16 * want.abs() + 1.01 * err + 1e-37).any()
+
+
 @pytest.mark.parametrize("K", [16, 144, 528])
 @pytest.mark.parametrize("T,N", SHAPES)
 @pytest.mark.parametrize("act", ["situv2", "silu"])
