@@ -401,9 +401,9 @@ typedef struct {
  *             (its rule applied to the fp32 values); dim % 32 == 0.  I8: codes [tokens, dim] and
  *             fp32 scales [tokens], as moe_quant_i8; dim % 16 == 0.  With q every given tensor of
  *             rows or channels is 16-byte aligned (else MOE_ERR_INVALID_ARG).
- * Shapes: 1 <= dim <= MOE_NORM_MAX_DIM (else MOE_ERR_UNSUPPORTED), any dim without q; rows of
- * dim % 8 == 0 elements on 16-byte aligned tensors take 16-byte accesses.  n, q and rstd's second
- * half need w_pre; w_post, a gate and rstd's first half need y; at least one output is given.
+ * Shapes: 1 <= dim <= MOE_NORM_MAX_DIM (else MOE_ERR_UNSUPPORTED), any dim without q.  n, q and
+ * rstd's second half need w_pre; w_post, a gate and rstd's first half need y; at least one output
+ * is given.
  * tokens == 0 returns MOE_OK.  Rows holding Inf or NaN give NaN in that row only. */
 moe_status_t moe_block_norm(const moe_block_norm_t *p, void *stream);
 

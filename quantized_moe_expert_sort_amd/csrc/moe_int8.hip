@@ -26,7 +26,6 @@ namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
 typedef int v16i __attribute__((ext_vector_type(16)));
-typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(2)));   // 8 bf16 of a row of any length
 
 // ---------------------------------------------------------------- coding of rows
 
@@ -390,12 +389,12 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
         const int c = cw + 16 * j + 8 * hl;
         if (t < p.T && c + 8 <= p.No) {
           if (p.add) {
-            const v4u_any q = *reinterpret_cast<const v4u_any*>(p.add + t * p.No + c);
+            float o[8];
+            load_any<8>(p.add + t * p.No + c, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] += __uint_as_float(i & 1 ? q[i / 2] & 0xFFFF0000u : q[i / 2] << 16);
+            for (int i = 0; i < 8; ++i) w[i] += o[i];
           }
-          *reinterpret_cast<v4u_any*>(p.out + t * p.No + c) =
-              v4u_any{bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
+          store_any<8>(p.out + t * p.No + c, w);
         } else if (t < p.T) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)

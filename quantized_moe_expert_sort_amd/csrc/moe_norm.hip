@@ -18,12 +18,13 @@
 // Measured on MI355X (a 2 GiB copy runs at 4.9 TB/s): forward 8192 x 3584 bf16 with fp8 codes 51 us
 // (265 MB: 54 us at the copy's rate), 4096 x 3584 with an fp32 stream 37 us (176 MB), one row 3.3 us;
 // backward 4096 x 3584, fp32 stream, gate per channel 48 us and 4.5 for the partial sums (264 MB).
+// Widths that 8 does not divide: 8192 x 3585 with a gate per element 46 us (36 at 3584), its backward
+// pass 86 (71); 4096 x 8191 57 (45) and 102 (77).
 // Rows of more than 8192 elements with a gate per channel spill in the backward pass (100 x 12000:
 // 41 us, 16 without the gate).
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
-#include <initializer_list>
 #include <type_traits>
 
 namespace moe {
@@ -96,12 +97,60 @@ __device__ __forceinline__ float sigmoid_f(float x) {
   return __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);
 }
 
-// The gate of this lane's VEC elements after its activation (GATE: what it is shared by).
-// row_gate: the row's gate with MOE_GATE_TOKEN.
+// VEC elements of a row of D from column `col`, at any address (global memory needs no alignment).
+// Where D is no multiple of 8 (SHORT) one lane's last piece is short: it reads the VEC elements that end with
+// the row and moves its own down, zeros behind them (own_part, only in the wave that holds that
+// piece).  Lanes past the row read the same ones, for others to replace.
+// Kernels of their own for SHORT rows: with the branch on it the backward pass of 8192 x 3584 took 54
+// us, 51.5 without; 8192 x 3585 takes 63 us, and 153 in single elements.
+template <int VEC, class T>
+__device__ __forceinline__ void load_at(const T* row, int col, int D, float (&v)[VEC]) {
+  load_any<VEC>(el(row, min(col, D - VEC)), v);
+}
+// Whether this wave holds the short piece, of lane `tr` of W waves a row; the same in all its lanes.
+template <int VEC, int CH>
+__device__ __forceinline__ bool holds_short(int W, int tr, int D) {
+  bool mine = false;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) mine |= c * W * 64 + tr == D / 8;
+  return __ballot(mine) != 0;
+}
+template <int VEC>
+__device__ __forceinline__ void own_part(int col, int D, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const bool last = col == (D & ~7);
+    const int shift = -D & 7;
+#pragma unroll
+    for (int b = 4; b > 0; b >>= 1)
+      if (shift & b) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = !last ? v[j] : j + b < 8 ? v[(j + b) & 7] : 0.0f;
+      }
+  }
+}
+template <int VEC, class T>
+__device__ __forceinline__ void load_own(const T* row, int col, int D, bool split, float (&v)[VEC]) {
+  load_at<VEC>(row, col, D, v);
+  if (split) own_part<VEC>(col, D, v);
+}
+// Stores the elements before D (col < D).
+template <int VEC, class T>
+__device__ __forceinline__ void store_own(T* row, int col, int D, bool split, const float (&v)[VEC]) {
+  if (!split || col + VEC <= D) {
+    store_any<VEC>(el(row, col), v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC - 1; ++j) {
+      const float one[1] = {v[j]};
+      if (col + j < D) store_row<1>(el(row, col + j), one);
+    }
+  }
+}
+
+// The gate of this lane's VEC elements after its activation (GATE: what it is shared by), from what
+// was loaded for them.  row_gate: the row's gate with MOE_GATE_TOKEN.
 template <int GATE, int VEC>
-__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t base, int col, float row_gate, float (&g)[VEC]) {
-  if constexpr (GATE == MOE_GATE_CHANNEL) load_row<VEC>(el(static_cast<const float*>(a.gate), col), g);
-  if constexpr (GATE == MOE_GATE_ELEMENT) load_row<VEC>(el(static_cast<const uint16_t*>(a.gate) + base, col), g);
+__device__ __forceinline__ void gate_values(const NormArgs& a, float row_gate, float (&g)[VEC]) {
   g[0] = GATE == MOE_GATE_NONE ? 1.0f : GATE == MOE_GATE_TOKEN ? row_gate : g[0];
   constexpr int n = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_ELEMENT ? VEC : 1;   // distinct values
   if (GATE != MOE_GATE_NONE && a.gate_act == MOE_GATE_SIGMOID) {
@@ -110,6 +159,12 @@ __device__ __forceinline__ void load_gate(const NormArgs& a, int64_t base, int c
   }
 #pragma unroll
   for (int j = n; j < VEC; ++j) g[j] = g[0];
+}
+template <int GATE, int VEC>
+__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t base, int col, float row_gate, bool split, float (&g)[VEC]) {
+  if constexpr (GATE == MOE_GATE_CHANNEL) load_own<VEC>(static_cast<const float*>(a.gate), col, a.D, split, g);
+  if constexpr (GATE == MOE_GATE_ELEMENT) load_own<VEC>(static_cast<const uint16_t*>(a.gate) + base, col, a.D, split, g);
+  gate_values<GATE, VEC>(a, row_gate, g);
 }
 
 // Codes of VEC = 8 consecutive elements; four adjacent lanes hold a block of 32 (inactive lanes
@@ -143,7 +198,7 @@ __device__ __forceinline__ void store_mx(const float (&v)[8], const NormArgs& a,
 
 // One row per W waves; R = blockDim.x / (64 W) rows per workgroup (R > 1 only with W == 1, so no
 // barrier is ever reached by part of a workgroup).
-template <int VEC, int CH, int GATE, class XT>
+template <int VEC, int CH, int GATE, bool SHORT, class XT>
 __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
   __shared__ float red[3][MAX_W];
   const int tr = W == 1 ? threadIdx.x & 63 : threadIdx.x;
@@ -153,21 +208,28 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
   const int64_t base = row * a.D;
   const XT* const x = static_cast<const XT*>(a.x);
   const float inv_d = 1.0f / (float)a.D;
+  const bool split = SHORT && holds_short<VEC, CH>(W, tr, a.D);
   // Lanes past the row read its last elements again and hold zeros: loads without branches, all of
   // them in flight together.
   float h[CH][VEC], y[CH][VEC];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) load_row<VEC>(el(x + base, min((c * W * 64 + tr) * VEC, a.D - VEC)), h[c]);
+  for (int c = 0; c < CH; ++c) load_at<VEC>(x + base, (c * W * 64 + tr) * VEC, a.D, h[c]);
   if (a.y) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) load_row<VEC>(el(a.y + base, min((c * W * 64 + tr) * VEC, a.D - VEC)), y[c]);
+    for (int c = 0; c < CH; ++c) load_at<VEC>(a.y + base, (c * W * 64 + tr) * VEC, a.D, y[c]);
   }
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
-    if ((c * W * 64 + tr) * VEC >= a.D) {
+  for (int c = 0; c < CH; ++c) {
+    const int col = (c * W * 64 + tr) * VEC;
+    if (split) {
+      own_part<VEC>(col, a.D, h[c]);
+      if (a.y) own_part<VEC>(col, a.D, y[c]);
+    }
+    if (col >= a.D) {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[c][j] = y[c][j] = 0.0f;
     }
+  }
   if (a.y) {
     float s[1] = {0.0f};
 #pragma unroll
@@ -187,22 +249,22 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
       const int col = (c * W * 64 + tr) * VEC;
       if (col < a.D) {
         float g[VEC], w[VEC];
-        load_gate<GATE, VEC>(a, base, col, row_gate, g);
+        load_gate<GATE, VEC>(a, base, col, row_gate, split, g);
         if (a.w_post) {
-          load_row<VEC>(el(a.w_post, col), w);
+          load_own<VEC>(a.w_post, col, a.D, split, w);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) y[c][j] *= w[j];
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) h[c][j] += k * g[j] * y[c][j];
-        if (a.h) store_row<VEC>(el(static_cast<XT*>(a.h) + base, col), h[c]);
+        if (a.h) store_own<VEC>(static_cast<XT*>(a.h) + base, col, a.D, split, h[c]);
       }
     }
   } else if (a.h) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * W * 64 + tr) * VEC;
-      if (col < a.D) store_row<VEC>(el(static_cast<XT*>(a.h) + base, col), h[c]);
+      if (col < a.D) store_own<VEC>(static_cast<XT*>(a.h) + base, col, a.D, split, h[c]);
     }
   }
   if (!a.w_pre) return;
@@ -221,10 +283,10 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
     const bool active = col < a.D;
     if (active) {
       float w[VEC];
-      load_row<VEC>(el(a.w_pre, col), w);
+      load_own<VEC>(a.w_pre, col, a.D, split, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[c][j] = h[c][j] * rh * w[j];
-      if (a.n) store_row<VEC>(el(a.n + base, col), h[c]);
+      if (a.n) store_own<VEC>(a.n + base, col, a.D, split, h[c]);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) h[c][j] = 0.0f;
@@ -258,7 +320,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
 // R rows at a time per workgroup, from blockIdx.x * R on, then every gridDim.x * R rows; all waves
 // make the same number of turns, so every barrier is reached by all of them.  Each workgroup
 // writes one partial row of the three sums over rows: [dw_pre | dw_post | dgate (per channel)].
-template <int VEC, int CH, int GATE, class XT>
+template <int VEC, int CH, int GATE, bool SHORT, class XT>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardArgs b, int W, int R) {
   __shared__ float red[2][2][2 * MAX_W];
   const NormArgs& a = b.f;
@@ -269,12 +331,13 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, has_dn = b.dn != nullptr, has_dh = b.dh != nullptr;
   const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
   constexpr bool fixed_gate = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_NONE;
+  const bool split = SHORT && holds_short<VEC, CH>(W, tr, a.D);
   float acc_pre[CH][VEC], acc_post[CH][VEC], acc_gate[CH][VEC], g[CH][VEC];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) acc_pre[c][j] = acc_post[c][j] = acc_gate[c][j] = 0.0f;
-    if constexpr (fixed_gate) load_gate<GATE, VEC>(a, 0, min((c * W * 64 + tr) * VEC, a.D - VEC), 1.0f, g[c]);
+    if constexpr (fixed_gate) load_gate<GATE, VEC>(a, 0, (c * W * 64 + tr) * VEC, 1.0f, split, g[c]);
   }
   // The norms' weights stay on chip: a row would wait for them once per use (three times 0.7 us).  Up
   // to 8 elements per lane in registers, else in LDS (one workgroup of 16 waves per CU as it is).
@@ -282,17 +345,17 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
   __shared__ float lds_w[IN_LDS ? 2 * MOE_NORM_MAX_DIM : 1];
   float w_post[IN_LDS ? 1 : CH][VEC], w_pre[IN_LDS ? 1 : CH][VEC];
   if constexpr (IN_LDS) {
-    for (int i = threadIdx.x; i < a.D; i += blockDim.x) {
-      lds_w[i] = post ? a.w_post[i] : 1.0f;
-      lds_w[MOE_NORM_MAX_DIM + i] = has_dn ? a.w_pre[i] : 0.0f;
+    for (int i = threadIdx.x; i < ((a.D + 7) & ~7); i += blockDim.x) {   // zeros past a row's end
+      lds_w[i] = i >= a.D ? 0.0f : post ? a.w_post[i] : 1.0f;
+      lds_w[MOE_NORM_MAX_DIM + i] = i < a.D && has_dn ? a.w_pre[i] : 0.0f;
     }
     lds_barrier();
   } else {
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int at = min((c * W * 64 + tr) * VEC, a.D - VEC);
-      if (post) load_row<VEC>(a.w_post + at, w_post[c]);
-      if (has_dn) load_row<VEC>(a.w_pre + at, w_pre[c]);
+      const int col = (c * W * 64 + tr) * VEC;
+      if (post) load_own<VEC>(a.w_post, col, a.D, split, w_post[c]);
+      if (has_dn) load_own<VEC>(a.w_pre, col, a.D, split, w_pre[c]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         w_post[c][j] = post ? w_post[c][j] : 1.0f;
@@ -300,10 +363,10 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
       }
     }
   }
-  // weights of the lane's elements of chunk c (columns from `at`)
-  const auto weights = [&](const float (&reg)[IN_LDS ? 1 : CH][VEC], int c, int at, int which, float (&w)[VEC]) {
+  // weights of the lane's elements of chunk c (columns from `col`)
+  const auto weights = [&](const float (&reg)[IN_LDS ? 1 : CH][VEC], int c, int col, int which, float (&w)[VEC]) {
     if constexpr (IN_LDS) {
-      load_row<VEC>(lds_w + which * MOE_NORM_MAX_DIM + at, w);
+      load_row<VEC>(lds_w + which * MOE_NORM_MAX_DIM + min(col, (a.D - 1) & ~(VEC - 1)), w);
     } else {
 #pragma unroll
       for (int j = 0; j < VEC; ++j) w[j] = reg[c][j];
@@ -325,16 +388,25 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     // the row hold zeros in h, y, u and e
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int at = min(c * W * 64 * VEC + lane_at, a.D - VEC);
-      load_row<VEC>(el(x + base, at), h[c]);
-      if (has_y) load_row<VEC>(el(a.y + base, at), y[c]);
-      if (has_dn) load_row<VEC>(el(b.dn + base, at), u[c]);
-      if (has_dh) load_row<VEC>(el(static_cast<const XT*>(b.dh) + base, at), e[c]);
-      if constexpr (!fixed_gate) load_gate<GATE, VEC>(a, base, at, row_gate, g[c]);
+      const int col = c * W * 64 * VEC + lane_at;
+      load_at<VEC>(x + base, col, a.D, h[c]);
+      if (has_y) load_at<VEC>(a.y + base, col, a.D, y[c]);
+      if (has_dn) load_at<VEC>(b.dn + base, col, a.D, u[c]);
+      if (has_dh) load_at<VEC>(static_cast<const XT*>(b.dh) + base, col, a.D, e[c]);
+      if constexpr (GATE == MOE_GATE_ELEMENT) load_at<VEC>(static_cast<const uint16_t*>(a.gate) + base, col, a.D, g[c]);
     }
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const bool out = c * W * 64 * VEC + lane_at >= a.D || !live;
+      const int col = c * W * 64 * VEC + lane_at;
+      const bool out = col >= a.D || !live;
+      if (split) {
+        own_part<VEC>(col, a.D, h[c]);
+        if (has_y) own_part<VEC>(col, a.D, y[c]);
+        if (has_dn) own_part<VEC>(col, a.D, u[c]);
+        if (has_dh) own_part<VEC>(col, a.D, e[c]);
+        if constexpr (GATE == MOE_GATE_ELEMENT) own_part<VEC>(col, a.D, g[c]);
+      }
+      if constexpr (!fixed_gate) gate_values<GATE, VEC>(a, row_gate, g[c]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         h[c][j] = out ? 0.0f : h[c][j];
@@ -346,7 +418,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     float s1[1] = {0.0f};
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int at = min(c * W * 64 * VEC + lane_at, a.D - VEC);
+      const int at = c * W * 64 * VEC + lane_at;
       if (has_y) {
         float w[VEC];
         weights(w_post, c, at, 0, w);
@@ -376,7 +448,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = c * W * 64 * VEC + lane_at;
-      if (live && col < a.D) store_row<VEC>(el(static_cast<XT*>(b.dx) + base, col), e[c]);
+      if (live && col < a.D) store_own<VEC>(static_cast<XT*>(b.dx) + base, col, a.D, split, e[c]);
     }
     if (!has_y) continue;
     float s2[2] = {0.0f, 0.0f};
@@ -384,7 +456,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     for (int c = 0; c < CH; ++c) {
       const int col = c * W * 64 * VEC + lane_at;
       float w[VEC], dg[VEC];
-      weights(w_post, c, min(col, a.D - VEC), 0, w);
+      weights(w_post, c, col, 0, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float se = a.scale * e[c][j];
@@ -400,7 +472,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
         }
       }
       if constexpr (GATE == MOE_GATE_ELEMENT)
-        if (live && col < a.D) store_row<VEC>(el(static_cast<uint16_t*>(b.dgate) + base, col), dg);
+        if (live && col < a.D) store_own<VEC>(static_cast<uint16_t*>(b.dgate) + base, col, a.D, split, dg);
     }
     if constexpr (GATE == MOE_GATE_TOKEN) {
       row_sums<2>(s2, red[parity][1], W, first);
@@ -415,7 +487,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
       if (live && col < a.D) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) u[c][j] = ry * (u[c][j] - y[c][j] * m);
-        store_row<VEC>(el(b.dy + base, col), u[c]);
+        store_own<VEC>(b.dy + base, col, a.D, split, u[c]);
       }
     }
   }
@@ -450,7 +522,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = (c * W * 64 + tr) * VEC;
-        if (col < a.D) store_row<VEC>(out + col, acc[c]);
+        if (col < a.D) store_own<VEC>(out, col, a.D, split, acc[c]);
       }
     }
   };
@@ -481,77 +553,63 @@ __global__ __launch_bounds__(1024) void norm_sum_parts_kernel(const float* __res
   }
 }
 
-// Elements per lane and access (8 where rows and pointers allow it, 2 in rows of even width, else
-// 1), in as few chunks as 16 waves hold.
+// 8 elements per lane and access in one or two chunks, as 16 waves hold them; one element in rows
+// of fewer than 8.
 struct Shape { int vec, ch, W, threads, R; };
-Shape norm_shape(int D, int vec) {
+Shape norm_shape(int D) {
   Shape s;
-  s.vec = vec;
-  const int per_wave = 64 * vec;
-  const int most = MAX_W * per_wave;                          // elements of one chunk
-  if (vec == 8) s.ch = D <= most ? 1 : 2;
-  else if (vec == 2) s.ch = D <= 2 * most ? 2 : D <= 4 * most ? 4 : 8;
-  else s.ch = D <= 4 * most ? 4 : 16;
-  s.W = (D + per_wave * s.ch - 1) / (per_wave * s.ch);
+  s.vec = D < 8 ? 1 : 8;
+  s.ch = D <= MAX_W * 512 ? 1 : 2;
+  const int per_wave = 64 * s.vec * s.ch;
+  s.W = (D + per_wave - 1) / per_wave;
   s.R = s.W == 1 ? 4 : 1;
   s.threads = 64 * s.W * s.R;
   return s;
 }
 
-// f(VEC, CH, GATE as integral constants, a value of the residual stream's type)
+// f(VEC, CH, GATE, SHORT as integral constants, a value of the residual stream's type)
 template <int V>
 using Const = std::integral_constant<int, V>;
 template <int VEC, int CH, class F>
 void norm_typed(const NormArgs& a, const F& f) {
-  const auto typed = [&](auto xt) {
+  const auto of_short = [&](auto is_short, auto xt) {
     switch (a.gate_kind) {
-      case MOE_GATE_CHANNEL: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_CHANNEL>(), xt); break;
-      case MOE_GATE_TOKEN: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_TOKEN>(), xt); break;
-      case MOE_GATE_ELEMENT: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_ELEMENT>(), xt); break;
-      default: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_NONE>(), xt); break;
+      case MOE_GATE_CHANNEL: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_CHANNEL>(), is_short, xt); break;
+      case MOE_GATE_TOKEN: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_TOKEN>(), is_short, xt); break;
+      case MOE_GATE_ELEMENT: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_ELEMENT>(), is_short, xt); break;
+      default: f(Const<VEC>(), Const<CH>(), Const<MOE_GATE_NONE>(), is_short, xt); break;
     }
+  };
+  const auto typed = [&](auto xt) {
+    if constexpr (VEC > 1) {
+      if (a.D % VEC) return of_short(std::true_type(), xt);
+    }
+    of_short(std::false_type(), xt);
   };
   if (a.x_dt == MOE_DT_F32) typed(float());
   else typed(uint16_t());
 }
 template <class F>
 void norm_dispatch(const NormArgs& a, const Shape& sh, const F& f) {
-  if (sh.vec == 8) {
-    if (sh.ch == 1) norm_typed<8, 1>(a, f);
-    else norm_typed<8, 2>(a, f);
-  } else if (sh.vec == 2) {
-    if (sh.ch == 2) norm_typed<2, 2>(a, f);
-    else if (sh.ch == 4) norm_typed<2, 4>(a, f);
-    else norm_typed<2, 8>(a, f);
-  } else {
-    if (sh.ch == 4) norm_typed<1, 4>(a, f);
-    else norm_typed<1, 16>(a, f);
-  }
+  if (sh.vec == 1) norm_typed<1, 1>(a, f);
+  else if (sh.ch == 1) norm_typed<8, 1>(a, f);
+  else norm_typed<8, 2>(a, f);
 }
-
-// The widest access that rows of D elements of every given tensor allow.
-int norm_vec(int D, std::initializer_list<const void*> ps) {
-  uintptr_t bits = 0;
-  for (const void* p : ps) bits |= (uintptr_t)p;
-  return D % 8 == 0 && !(bits & 15) ? 8 : D % 2 == 0 && !(bits & 7) ? 2 : 1;
-}
-const void* wide_gate(const NormArgs& a) { return a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate; }
 
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
-  const Shape sh = norm_shape(a.D, norm_vec(a.D, {a.x, a.y, a.w_post, wide_gate(a), a.w_pre, a.h, a.n, a.q}));
+  const Shape sh = norm_shape(a.D);
   const unsigned grid = (unsigned)((a.T + sh.R - 1) / sh.R);
-  norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto xt) {
-    norm_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, sh.threads, 0, s>>>(a, sh.W);
+  norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto is_short, auto xt) {
+    norm_kernel<vec(), ch(), gate(), is_short(), decltype(xt)><<<grid, sh.threads, 0, s>>>(a, sh.W);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_block_norm_backward(const NormBackwardArgs& b, hipStream_t s) {
   const NormArgs& a = b.f;
-  const Shape sh = norm_shape(a.D, norm_vec(a.D, {a.x, a.y, a.w_post, wide_gate(a), a.w_pre, b.dh, b.dn, b.dx, b.dy,
-                                                  a.gate_kind == MOE_GATE_ELEMENT ? b.dgate : nullptr, b.part}));
+  const Shape sh = norm_shape(a.D);
   // Beyond a row per workgroup, as many rows at a time as 16 waves take: fewer partial sums than
   // with more workgroups of fewer waves (4096 x 3584: 54 us, 60 with 512 workgroups; 9000 x 130: 14, 17)
   const int want = (a.T + MOE_NORM_PARTS - 1) / MOE_NORM_PARTS, fit = sh.ch * sh.vec > 8 ? 1 : MAX_W / sh.W;
@@ -559,8 +617,8 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& b, hipStream_t s) 
   const int groups = R > 0 ? (a.T + R - 1) / R : 0;
   const unsigned grid = (unsigned)(groups < MOE_NORM_PARTS ? groups : MOE_NORM_PARTS);
   if (grid > 0) {                                             // no rows: the sums below are zero
-    norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto xt) {
-      norm_backward_kernel<vec(), ch(), gate(), decltype(xt)><<<grid, 64 * sh.W * R, 0, s>>>(b, sh.W, R);
+    norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto is_short, auto xt) {
+      norm_backward_kernel<vec(), ch(), gate(), is_short(), decltype(xt)><<<grid, 64 * sh.W * R, 0, s>>>(b, sh.W, R);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

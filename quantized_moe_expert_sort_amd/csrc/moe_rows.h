@@ -37,8 +37,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) { return cross_row_
 
 // ------------------------------------------------------------------ VEC elements of a row
 //
-// VEC 8: 16-byte accesses (rows and base pointers 16-byte aligned); VEC 2: pairs; VEC 1: single
-// elements, for widths and pointers that no wide access divides.
+// load_row, store_row: VEC 8 in 16-byte accesses (addresses 16-byte aligned), VEC 1 single elements.
 
 typedef float v4f_ __attribute__((ext_vector_type(4)));
 typedef uint32_t v4u_ __attribute__((ext_vector_type(4)));
@@ -52,10 +51,6 @@ __device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[VEC]) {
       v[2 * j] = __uint_as_float(q[j] << 16);
       v[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
     }
-  } else if constexpr (VEC == 2) {
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(p);
-    v[0] = __uint_as_float(q << 16);
-    v[1] = __uint_as_float(q & 0xFFFF0000u);
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float((uint32_t)p[j] << 16);
@@ -70,10 +65,6 @@ __device__ __forceinline__ void load_row(const float* p, float (&v)[VEC]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[4 * j + i] = q[i];
     }
-  } else if constexpr (VEC == 2) {
-    const float2 q = *reinterpret_cast<const float2*>(p);
-    v[0] = q.x;
-    v[1] = q.y;
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = p[j];
@@ -91,8 +82,6 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[VEC]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
     *reinterpret_cast<v4u_*>(p) = q;
-  } else if constexpr (VEC == 2) {
-    *reinterpret_cast<uint32_t*>(p) = bf16_pair(v[0], v[1]);
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) p[j] = __builtin_bit_cast(uint16_t, (__bf16)v[j]);
@@ -103,11 +92,62 @@ __device__ __forceinline__ void store_row(float* p, const float (&v)[VEC]) {
   if constexpr (VEC % 4 == 0) {
 #pragma unroll
     for (int j = 0; j < VEC / 4; ++j) reinterpret_cast<v4f_*>(p)[j] = v4f_{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
-  } else if constexpr (VEC == 2) {
-    *reinterpret_cast<float2*>(p) = float2{v[0], v[1]};
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) p[j] = v[j];
+  }
+}
+
+// load_any, store_any: the same at any address of global memory, which needs no alignment beyond an
+// element's: the hardware takes the wide accesses apart where they cross lines.
+typedef float v4f_any_ __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v4u_any_ __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int VEC>
+__device__ __forceinline__ void load_any(const uint16_t* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    const v4u_any_ q = *reinterpret_cast<const v4u_any_*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(q[j] << 16);
+      v[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+    }
+  } else {
+    load_row<VEC>(p, v);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void load_any(const float* p, float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const v4f_any_ q = reinterpret_cast<const v4f_any_*>(p)[j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[4 * j + i] = q[i];
+    }
+  } else {
+    load_row<VEC>(p, v);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_any(uint16_t* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+    v4u_any_ q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+    *reinterpret_cast<v4u_any_*>(p) = q;
+  } else {
+    store_row<VEC>(p, v);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void store_any(float* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 8) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      reinterpret_cast<v4f_any_*>(p)[j] = v4f_any_{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]};
+  } else {
+    store_row<VEC>(p, v);
   }
 }
 

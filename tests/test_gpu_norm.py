@@ -91,6 +91,28 @@ def test_combinations(x_dt, kind, act, post, pre):
     check(6, 333, x_dt, kind, act, post, pre, dn=pre, seed=1)
 
 
+@pytest.mark.parametrize("D", [9, 10, 11, 12, 13, 14, 15, 505, 513, 519, 1023, 4095, 8185, 8191, 8193, 8199, 16383])
+@pytest.mark.parametrize("kind", ["channel", "element"])
+def test_every_length_of_a_rows_last_piece(D, kind):
+    check(5, D, kind=kind, act="sigmoid")
+    check(5, D, torch.float32, kind=kind, shift=1)
+
+
+@pytest.mark.parametrize("x_dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,D", [(5, 11), (3, 517), (4, 5127), (2, 9001)])
+def test_in_place_with_a_short_last_piece(T, D, x_dt):
+    # the last elements of a row are read together with ones that other lanes store to
+    d = gpu(make(T, D, x_dt, "element", "sigmoid", seed=4))
+    kw = dict(w_post=d["w_post"], gate=d["gate"], gate_kind="element", gate_act="sigmoid", scale=0.5, w_pre=d["w_pre"])
+    r = qm.moe_block_norm(d["x"], d["y"], **kw)
+    buf = torch.full((T + 2, D), 7.0, dtype=x_dt, device="cuda")
+    for _ in range(5):
+        buf[1:-1].copy_(d["x"])
+        q = qm.moe_block_norm(buf[1:-1], d["y"], h=buf[1:-1], **kw)
+        assert torch.equal(q.h, r.h) and torch.equal(q.n, r.n)
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+
+
 @pytest.mark.parametrize("dh,dn", [(True, False), (False, True)])
 def test_one_gradient_only(dh, dn):
     check(9, 640, kind="channel", dh=dh, dn=dn)
@@ -152,6 +174,22 @@ def test_rows_with_infinity_or_nan_stay_to_themselves():
     assert torch.equal(r.n[keep], s.n[keep]) and torch.equal(r.q[keep], s.q[keep])
     assert torch.isnan(r.n[1]).any() and torch.isnan(r.n[3]).all()
     assert torch.isnan(r.q_scale[[1, 3]]).all() and (r.q[[1, 3]] == 0).all()
+
+
+@pytest.mark.parametrize("D", [13, 515, 8195])
+def test_the_end_of_a_row_does_not_see_the_next(D):
+    c = make(4, D, kind="element", act="sigmoid", seed=5)
+    for k in ("x", "y", "gate", "dh", "dn"):
+        c[k][1] = c[k][3] = float("nan")
+    d = gpu(c)
+    kw = dict(w_post=d["w_post"], gate_kind="element", gate_act="sigmoid", w_pre=d["w_pre"])
+    r = qm.moe_block_norm(d["x"], d["y"], gate=d["gate"], stats=True, **kw)
+    b = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, d["dh"], d["dn"], gate=d["gate"], **kw)
+    one = {k: d[k][[0, 2]].contiguous() for k in ("x", "y", "gate", "dh", "dn")}
+    r1 = qm.moe_block_norm(one["x"], one["y"], gate=one["gate"], stats=True, **kw)
+    b1 = qm.moe_block_norm_backward(one["x"], one["y"], r1.rstd, one["dh"], one["dn"], gate=one["gate"], **kw)
+    for got, want in ((r.h, r1.h), (r.n, r1.n), (b.dx, b1.dx), (b.dy, b1.dy), (b.dgate, b1.dgate)):
+        assert torch.equal(got[[0, 2]], want) and got[[1, 3]].isnan().all()
 
 
 @pytest.mark.parametrize("D", [96, 97])
