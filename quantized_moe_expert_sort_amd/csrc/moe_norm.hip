@@ -20,8 +20,8 @@
 // backward 4096 x 3584, fp32 stream, gate per channel 48 us and 4.5 for the partial sums (264 MB).
 // Widths that 8 does not divide: 8192 x 3585 with a gate per element 46 us (36 at 3584), its backward
 // pass 86 (71); 4096 x 8191 57 (45) and 102 (77).
-// Rows of more than 8192 elements with a gate per channel spill in the backward pass (100 x 12000:
-// 41 us, 16 without the gate).
+// Rows of more than 8192 elements fill a lane's 128 registers in the backward pass (about 14 spilled
+// with a gate per channel or element): 1000 x 12000 bf16 41 and 45 us, 31 without a gate.
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
@@ -332,11 +332,13 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
   const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
   constexpr bool fixed_gate = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_NONE;
   const bool split = SHORT && holds_short<VEC, CH>(W, tr, a.D);
-  float acc_pre[CH][VEC], acc_post[CH][VEC], acc_gate[CH][VEC], g[CH][VEC];
+  // acc_post: sum of dz yh, or with a gate per channel of scale e yh, which gives both dw_post (times
+  // g) and the gate's gradient (times w_post and the activation's slope) after the last row
+  float acc_pre[CH][VEC], acc_post[CH][VEC], g[CH][VEC];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) acc_pre[c][j] = acc_post[c][j] = acc_gate[c][j] = 0.0f;
+    for (int j = 0; j < VEC; ++j) acc_pre[c][j] = acc_post[c][j] = 0.0f;
     if constexpr (fixed_gate) load_gate<GATE, VEC>(a, 0, (c * W * 64 + tr) * VEC, 1.0f, split, g[c]);
   }
   // The norms' weights stay on chip: a row would wait for them once per use (three times 0.7 us).  Up
@@ -462,12 +464,11 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
         const float se = a.scale * e[c][j];
         const float dz = se * g[c][j];
         u[c][j] = dz * w[j];
-        acc_post[c][j] += dz * y[c][j];
+        acc_post[c][j] += (GATE == MOE_GATE_CHANNEL ? se : dz) * y[c][j];
         s2[0] += u[c][j] * y[c][j];
-        if constexpr (GATE != MOE_GATE_NONE) {
+        if constexpr (GATE == MOE_GATE_TOKEN || GATE == MOE_GATE_ELEMENT) {
           dg[j] = se * (y[c][j] * w[j]);
           if (sigmoid) dg[j] *= g[c][j] * (1.0f - g[c][j]);
-          if constexpr (GATE == MOE_GATE_CHANNEL) acc_gate[c][j] += dg[j];
           if constexpr (GATE == MOE_GATE_TOKEN) s2[1] += dg[j];
         }
       }
@@ -527,8 +528,21 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     }
   };
   if (b.dw_pre) finish(acc_pre, part);
+  if constexpr (GATE == MOE_GATE_CHANNEL) {
+    float dg[CH][VEC];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[VEC];
+      weights(w_post, c, (c * W * 64 + tr) * VEC, 0, w);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        dg[c][j] = acc_post[c][j] * (sigmoid ? w[j] * g[c][j] * (1.0f - g[c][j]) : w[j]);
+        acc_post[c][j] *= g[c][j];
+      }
+    }
+    finish(dg, part + 2 * (int64_t)a.D);
+  }
   if (b.dw_post) finish(acc_post, part + a.D);
-  if constexpr (GATE == MOE_GATE_CHANNEL) finish(acc_gate, part + 2 * (int64_t)a.D);
 }
 
 // out_k[col] = sum over the partial rows, for the sums that are asked for (blockIdx.y = k).
