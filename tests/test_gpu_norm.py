@@ -176,6 +176,26 @@ def test_rows_with_infinity_or_nan_stay_to_themselves():
     assert torch.isnan(r.q_scale[[1, 3]]).all() and (r.q[[1, 3]] == 0).all()
 
 
+@pytest.mark.parametrize("T,D", [(7, 11), (600, 515), (3, 5127), (300, 8200)])
+def test_backward_over_its_own_gradient(T, D, monkeypatch):
+    # dx may be dh
+    d = gpu(make(T, D, kind="channel", act="sigmoid", seed=6))
+    kw = dict(w_post=d["w_post"], gate=d["gate"], gate_kind="channel", gate_act="sigmoid", w_pre=d["w_pre"])
+    r = qm.moe_block_norm(d["x"], d["y"], stats=True, **kw)
+    b = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, d["dh"], d["dn"], **kw)
+    call = qm._call
+
+    def over_dh(name, index, p, g, *rest):
+        g.dx = g.dh
+        return call(name, index, p, g, *rest)
+    monkeypatch.setattr(qm, "_call", over_dh)
+    dh = d["dh"].clone()
+    o = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, dh, d["dn"], **kw)
+    assert torch.equal(dh, b.dx)
+    for got, want in zip(o[1:], b[1:]):
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("D", [13, 515, 8195])
 def test_the_end_of_a_row_does_not_see_the_next(D):
     c = make(4, D, kind="element", act="sigmoid", seed=5)
