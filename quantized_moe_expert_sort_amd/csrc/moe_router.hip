@@ -138,12 +138,11 @@ __device__ __forceinline__ double exact_sum(const LT* row, int E, float m, int l
   }
   return wave_sum_f64(s);
 }
-// K maxima over the wave, each over every key that is left.
-template <class LT, bool BIAS>
+// With a bias: K maxima over the wave, each over every key that is left, in 64 bits.
+template <class LT>
 __device__ __forceinline__ void choose_in_rounds(const LT* row, const float* bias, int E, int K, int score, float m,
                                                  int lane, int& id, float& logit) {
-  double zd = 1.0;
-  if (BIAS && score == MOE_SCORE_SOFTMAX) zd = exact_sum(row, E, m, lane);
+  const double zd = score == MOE_SCORE_SOFTMAX ? exact_sum(row, E, m, lane) : 1.0;
   uint32_t taken = 0;                                         // E <= 64 * 32
 #pragma unroll 1
   for (int r = 0; r < K; ++r) {
@@ -155,12 +154,8 @@ __device__ __forceinline__ void choose_in_rounds(const LT* row, const float* bia
       float v[1];
       load_row<1>(row + e, v);
       const float l = sane(v[0]);
-      if (!(l > -INFINITY) || ((taken >> i) & 1)) continue;
-      double k = (double)l;
-      if constexpr (BIAS) {
-        if (!(bias[e] > -INFINITY)) continue;
-        k = exact_key(l, __builtin_fminf(bias[e], BIG), score, m, zd);
-      }
+      if (!(l > -INFINITY) || !(bias[e] > -INFINITY) || ((taken >> i) & 1)) continue;
+      const double k = exact_key(l, __builtin_fminf(bias[e], BIG), score, m, zd);
       if (wc == 0x7FFFFFFF || k > wk) { wk = k; wc = e; wl = l; }
     }
 #pragma unroll
@@ -174,6 +169,83 @@ __device__ __forceinline__ void choose_in_rounds(const LT* row, const float* bia
     if ((wc & 63) == lane) taken |= 1u << (wc >> 6);
     if (lane == r) { id = wc; logit = wl; }
   }
+}
+
+// The fp32 keys with a bias are off by less than half of this: a score by 4e-6 at most (the rounding
+// of the exponents, of the sum of up to 2048 exponentials and of the quotient), the sum of score and
+// bias by 2^-24 of itself.  So every expert among the K largest exact keys has an fp32 key of at least
+// bound - key_margin(bound), where K fp32 keys reach the bound.
+__device__ __forceinline__ float key_margin(float bound) { return 1e-5f * (1.0f + __builtin_fabsf(bound)); }
+
+// The candidates of a row that has more than CAND experts above the ordinary bound (many ties, a K near
+// half the lanes): those that reach the K-th largest key, of experts with the same logit and bias as it
+// only the K with the lowest numbers (the others cannot be chosen).  Returns how many; the first CAND
+// of them are in cand.  Without a bias they are fewer than 2 K <= CAND.
+// 3400 x 2048, K 32 (about one row in 50 comes here) 22 us, 172 with K maxima over the whole row
+// instead; 16384 x 896 of zeros (every row comes here) 32 us.
+template <class LT, int VEC, int NREG, bool BIAS>
+__device__ __forceinline__ int collect_from_kth(const LT* row, const float (&l)[NREG], const float (&keys)[BIAS ? NREG : 1],
+                                                const float* bias, int E, int K, int score, float m, float z,
+                                                float best, uint2* cand, int lane) {
+  const auto key = [&](int i) { return BIAS ? keys[i] : l[i]; };
+  const auto reach = [&](float v) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) n += __popcll(__ballot(key(i) >= v));
+    return n;
+  };
+  // The largest key where K have it (rows of equal logits); else from the top bit down, until just K
+  // reach it.
+  float kth = wave_max(best);
+  if (reach(kth) < K) {
+    uint32_t t = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const int n = reach(unordered(t | (1u << bit)));
+      if (n >= K) t |= 1u << bit;
+      if (n == K) break;
+    }
+    kth = unordered(t);
+  }
+  const float bound = BIAS ? __builtin_fmaxf(kth - key_margin(kth), -BIG) : kth;
+  bool ties = !BIAS;                                          // whether an expert with this very key was found
+  float tied_l = kth, tied_b = 0.0f;
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int i = 0; i < NREG; ++i) {
+      const uint64_t mask = __ballot(keys[i] == kth);
+      if (mask && !ties) {
+        const int from = __builtin_ctzll(mask);
+        ties = true;
+        tied_l = readlane_f(l[i], from);
+        tied_b = __builtin_fminf(bias[column<VEC>(i, from)], BIG);
+      }
+    }
+  }
+  int n = 0, same = 0;
+#pragma unroll 1
+  for (int e = lane; e - lane < E; e += 64) {                 // in the experts' order
+    const int at = min(e, E - 1);
+    float v[1];
+    load_row<1>(row + at, v);
+    const float x = e < E ? sane(v[0]) : -INFINITY;
+    float k = x, b = 0.0f;
+    if constexpr (BIAS) {
+      const bool left = x > -INFINITY && bias[at] > -INFINITY;
+      b = __builtin_fminf(bias[at], BIG);
+      k = left ? (score == MOE_SCORE_SOFTMAX ? exp_f(x - m) / z : fast_sigmoid(x)) + b : -INFINITY;
+    }
+    const bool tied = ties && k > -INFINITY && x == tied_l && b == tied_b;
+    const uint64_t all = __ballot(tied);
+    const int before = same + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0));
+    same += __popcll(all);
+    const bool in = tied ? before < K : k >= bound;
+    const uint64_t mask = __ballot(in);
+    const int p = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+    if (in && p < CAND) cand[p] = uint2{__float_as_uint(x), (uint32_t)e};
+    n += __popcll(mask);
+  }
+  return n;
 }
 
 // One wave's row: on return lane r < K holds the expert of rank r (ascending rank) and its logit, or
@@ -214,14 +286,8 @@ __device__ __forceinline__ void choose(const LT* row, const float (&l)[NREG], fl
     }
   }
   float bound = t ? unordered(t) : -BIG;
-  float margin = 0.0f;
   if constexpr (BIAS) {
-    // The fp32 keys are off by less than margin / 2: a score by 4e-6 at most (the rounding of the
-    // exponents, of the sum of up to 2048 exponentials and of the quotient), the sum of score and
-    // bias by 2^-24 of itself.  So every expert among the K largest exact keys has an fp32 key of
-    // at least bound - margin.
-    margin = 1e-5f * (1.0f + __builtin_fabsf(bound));
-    bound = __builtin_fmaxf(bound - margin, -BIG);
+    bound = __builtin_fmaxf(bound - key_margin(bound), -BIG);
   }
   int n = 0;
 #pragma unroll
@@ -235,62 +301,68 @@ __device__ __forceinline__ void choose(const LT* row, const float (&l)[NREG], fl
     }
   }
   wave_sync();
-  if (n <= CAND) {
-    const bool have = lane < n;
-    const uint2 c = have ? cand[lane] : uint2{0xFF800000u, 0x7FFFFFFFu};
-    const float cl = __uint_as_float(c.x);
-    int rank = 0;
-    if constexpr (BIAS) {
-      const float b = have ? __builtin_fminf(bias[c.y], BIG) : 0.0f;
-      double k = 0.0, zd = 1.0;
-      bool done = false;
-      if (score == MOE_SCORE_SOFTMAX) {
-        // fp32 keys decide unless two of them are close: the sum in 64 bits costs more than the rest
-        const float k32 = exp_f(cl - m) / z + b;
-        bool close = false;
-        for (int j = 0; j < n; ++j) {
-          const float o = readlane_f(k32, j);
-          rank += o > k32;
-          close |= j != lane && __builtin_fabsf(o - k32) <= 1e-5f * (1.0f + __builtin_fabsf(k32));
-        }
-        done = __ballot(have && close) == 0;
-        if (!done) zd = exact_sum(row, E, m, lane);
-      }
-      if (!done) {
-        rank = 0;
-        if (have) k = exact_key(cl, b, score, m, zd);
-        for (int j = 0; j < n; ++j) {
-          const double o = readlane_d(k, j);
-          const int oc = __builtin_amdgcn_readlane((int)c.y, j);
-          rank += o > k || (o == k && oc < (int)c.y);
-        }
-      }
-    } else if constexpr (sizeof(LT) == 2) {
-      // bf16: the upper half of the ordered key says it all (rounded up, so that a clamped +inf, the one
-      // value that is no bf16, stays above the largest bf16), the column goes below it
-      const uint32_t k = ((ordered(cl) + 0xFFFFu) & 0xFFFF0000u) | (0xFFFFu - (c.y & 0xFFFFu));
-      for (int j = 0; j < n; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)k, j) > k;
-    } else {
-      const uint64_t k = ((uint64_t)ordered(cl) << 32) | (0xFFFFFFFFu - c.y);
-      for (int j = 0; j < n; ++j) {
-        const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), j) << 32) |
-                           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
-        rank += o > k;
-      }
-    }
-    // to the lane of its rank (ranks of the candidates are 0 .. n - 1, each once)
+  if (n > CAND) {
+    n = collect_from_kth<LT, VEC, NREG, BIAS>(row, l, keys, bias, E, K, score, m, z, best, cand, lane);
     wave_sync();
-    if (have) cand[rank] = c;
-    wave_sync();
-    if (lane < min(n, K)) {
-      const uint2 r = cand[lane];
-      id = (int)r.y;
-      logit = __uint_as_float(r.x);
-    }
-    wave_sync();
-    return;
   }
-  choose_in_rounds<LT, BIAS>(row, bias, E, K, score, m, lane, id, logit);   // more than 64 candidates
+  if constexpr (BIAS) {
+    if (n > CAND) {                                           // keys closer than their error
+      choose_in_rounds(row, bias, E, K, score, m, lane, id, logit);
+      return;
+    }
+  }
+  const bool have = lane < n;
+  const uint2 c = have ? cand[lane] : uint2{0xFF800000u, 0x7FFFFFFFu};
+  const float cl = __uint_as_float(c.x);
+  int rank = 0;
+  if constexpr (BIAS) {
+    const float b = have ? __builtin_fminf(bias[c.y], BIG) : 0.0f;
+    double k = 0.0, zd = 1.0;
+    bool done = false;
+    if (score == MOE_SCORE_SOFTMAX) {
+      // fp32 keys decide unless two of them are close: the sum in 64 bits costs more than the rest
+      const float k32 = exp_f(cl - m) / z + b;
+      bool close = false;
+      for (int j = 0; j < n; ++j) {
+        const float o = readlane_f(k32, j);
+        rank += o > k32;
+        close |= j != lane && __builtin_fabsf(o - k32) <= 1e-5f * (1.0f + __builtin_fabsf(k32));
+      }
+      done = __ballot(have && close) == 0;
+      if (!done) zd = exact_sum(row, E, m, lane);
+    }
+    if (!done) {
+      rank = 0;
+      if (have) k = exact_key(cl, b, score, m, zd);
+      for (int j = 0; j < n; ++j) {
+        const double o = readlane_d(k, j);
+        const int oc = __builtin_amdgcn_readlane((int)c.y, j);
+        rank += o > k || (o == k && oc < (int)c.y);
+      }
+    }
+  } else if constexpr (sizeof(LT) == 2) {
+    // bf16: the upper half of the ordered key says it all (rounded up, so that a clamped +inf, the one
+    // value that is no bf16, stays above the largest bf16), the column goes below it
+    const uint32_t k = ((ordered(cl) + 0xFFFFu) & 0xFFFF0000u) | (0xFFFFu - (c.y & 0xFFFFu));
+    for (int j = 0; j < n; ++j) rank += (uint32_t)__builtin_amdgcn_readlane((int)k, j) > k;
+  } else {
+    const uint64_t k = ((uint64_t)ordered(cl) << 32) | (0xFFFFFFFFu - c.y);
+    for (int j = 0; j < n; ++j) {
+      const uint64_t o = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), j) << 32) |
+                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, j);
+      rank += o > k;
+    }
+  }
+  // to the lane of its rank (ranks of the candidates are 0 .. n - 1, each once)
+  wave_sync();
+  if (have) cand[rank] = c;
+  wave_sync();
+  if (lane < min(n, K)) {
+    const uint2 r = cand[lane];
+    id = (int)r.y;
+    logit = __uint_as_float(r.x);
+  }
+  wave_sync();
 }
 
 // ws of the balance statistics: [256] a ticket, [parts] Tv, [parts] z sums, [ceil(E / 64)] loss

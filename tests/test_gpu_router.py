@@ -116,6 +116,42 @@ def test_equal_keys_go_to_the_lowest_expert(E, with_bias, score):
         check(logits, min(E, 16), score, bias=bias, z_coef=0.0 if logits.min() < -1e30 else 0.02)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,K", [(100, 32), (130, 31), (512, 32), (800, 28), (1023, 32), (1024, 31), (1536, 32), (2048, 32)])
+def test_rows_with_many_candidates(E, K, dt):
+    # with K near half the lanes the lanes' maxima bound the choice so loosely that more than 64 experts
+    # pass; among 300 rows some do at each of these sizes
+    logits, g = make(300, E, dt)
+    check(logits, K, train=False)
+    check(logits, K, "sigmoid", bias=0.1 * torch.randn(E, generator=g), train=False)
+    check(logits, K, "softmax", bias=0.01 * torch.randn(E, generator=g), train=False)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [96, 200, 500, 896, 1021, 2048])
+def test_rows_of_ties(E, dt):
+    g = torch.Generator().manual_seed(E)
+    flat = torch.zeros(8, E)
+    flat[1] = -3.5
+    flat[2] = 3e38                                             # all at the top
+    flat[3, ::2] = -0.0                                        # equal to 0
+    flat[4] = torch.randint(0, 2, (E,), generator=g).float()   # two values
+    flat[5] = torch.randint(0, 2, (E,), generator=g).float() - 1
+    flat[6] = 1.0
+    flat[6, torch.randperm(E, generator=g)[:7]] = 2.0          # a few above the ties
+    flat[7, torch.randperm(E, generator=g)[:E // 2]] = float("-inf")
+    flat = flat.to(dt)
+    levels = torch.randint(0, 3, (E,), generator=g).float() / 4
+    masked = levels.clone()
+    masked[::3] = float("nan")
+    masked[1::5] = float("-inf")
+    for K in (1, 8, 32):
+        check(flat, K, train=False)
+        for bias in (torch.zeros(E), levels, masked):
+            check(flat, K, "sigmoid", bias=bias, train=False)
+            check(flat, K, "softmax", bias=bias, train=False)
+
+
 def test_keys_that_32_bits_cannot_order():
     # pairs of experts whose keys differ by 1e-9: fp32 rounds them to the same value or swaps them
     E, T = 64, 200
