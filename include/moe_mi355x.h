@@ -353,7 +353,8 @@ moe_status_t moe_fused_noalloc(const void *x, const uint8_t *x_scale, int32_t a_
 /* ---------------------------------------------------------------------------------------------
  * The rest of the layer: the norms before and after a block, the router with its balance loss,
  * and the 8-bit integer product of a shared expert.  The conventions above hold for these too.
- * Optional pointers are NULL when not given.  Outputs must not overlap inputs or each other
+ * Optional pointers are NULL when not given.  A workspace that a call reads is 4-byte aligned (else
+ * MOE_ERR_INVALID_ARG).  Outputs must not overlap inputs or each other
  * except where a call allows it.  All sums, statistics and partial sums are fp32 (int32 for the
  * integer product), no call uses atomics whose order changes a result, and equal calls on equal
  * devices give equal bits.

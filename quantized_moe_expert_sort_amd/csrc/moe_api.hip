@@ -285,6 +285,8 @@ moe_status_t moe_fused_noalloc(const void* x, const uint8_t* x_scale, int32_t a_
 namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+// Workspaces of 4-byte words: an atomic on a misaligned one would be a memory fault.
+bool aligned4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 bool row_type(int32_t dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_F32; }
 
 // What the forward and the backward pass of the block norm both require; *a is filled.
@@ -357,7 +359,7 @@ moe_status_t moe_block_norm_backward(const moe_block_norm_t* p, const moe_block_
   if (some && (d->dw_pre == nullptr) != (d->dn == nullptr)) return MOE_ERR_INVALID_ARG;
   if (d->dn && !p->w_pre) return MOE_ERR_INVALID_ARG;
   if (some && (p->w_post || d->dn) && !p->rstd) return MOE_ERR_INVALID_ARG;
-  if (some && !ws) return MOE_ERR_INVALID_ARG;
+  if (some && (!ws || !aligned4(ws))) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_block_norm_backward_ws_bytes(p->tokens, p->dim)) return MOE_ERR_WORKSPACE;
   b.dh = d->dh;
   b.dn = d->dn;
@@ -377,7 +379,7 @@ moe_status_t moe_router(const moe_router_t* r, const moe_balance_t* balance, voi
   if (st != MOE_OK) return st;
   if (r->tokens > 0 && (!r->topk_ids || !r->topk_w)) return MOE_ERR_INVALID_ARG;
   if (balance) {
-    if (!b.counts || !b.mean_prob || !b.loss || !b.num_valid || !ws) return MOE_ERR_INVALID_ARG;
+    if (!b.counts || !b.mean_prob || !b.loss || !b.num_valid || !ws || !aligned4(ws)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < moe_router_ws_bytes(r->num_experts)) return MOE_ERR_WORKSPACE;
   } else if (r->tokens == 0) {
     return MOE_OK;

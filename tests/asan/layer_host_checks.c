@@ -48,6 +48,7 @@ static void norm_checks(void) {
   d->dh = P; d->dx = P; d->dy = P; d->dw_post = P;
   EXPECT(moe_block_norm_backward(p, d, P, 16, NULL), MOE_ERR_WORKSPACE);
   EXPECT(moe_block_norm_backward(p, d, NULL, 1 << 20, NULL), MOE_ERR_INVALID_ARG);
+  EXPECT(moe_block_norm_backward(p, d, (char *)P + 2, 1 << 20, NULL), MOE_ERR_INVALID_ARG);
   free(d); free(p);
 }
 
@@ -65,6 +66,7 @@ static void router_checks(void) {
   EXPECT(moe_router(r, b, P, 1 << 20, NULL), MOE_ERR_INVALID_ARG);
   b->counts = P; b->mean_prob = P; b->loss = P; b->num_valid = P;
   EXPECT(moe_router(r, b, P, 16, NULL), MOE_ERR_WORKSPACE);
+  EXPECT(moe_router(r, b, (char *)P + 1, 1 << 20, NULL), MOE_ERR_INVALID_ARG);
   EXPECT(moe_router_backward(r, NULL, NULL, NULL, P, NULL), MOE_ERR_INVALID_ARG);
   EXPECT(moe_router_backward(r, b, P, NULL, NULL, NULL), MOE_ERR_INVALID_ARG);
   r->tokens = 0;

@@ -198,3 +198,15 @@ def test_binding_refuses_tensors_off_the_gpu_and_unknown_names():
         qm._router_params(x, 2, "sigmoid", True, 1.0, torch.zeros(63), None, dev)
     with pytest.raises(ValueError, match="logits"):
         qm._router_params(x.half(), 2, "sigmoid", True, 1.0, None, None, dev)
+
+
+@no_gpu
+def test_workspaces_have_to_be_aligned_like_their_words():
+    # the workspaces hold 4-byte words, among them one that is counted up by atomics
+    need = qm.router_ws_bytes(8)
+    for off in (1, 2, 3):
+        assert qm.lib().moe_router(router(), qm.BalanceParams(**BAL), P + off, need, None) == INVALID, off
+        assert qm.lib().moe_router(router(tokens=0), qm.BalanceParams(**BAL), P + off, need, None) == INVALID, off
+        assert backward_status(ws=P + off) == INVALID, off
+        # where no workspace is read, its address does not matter
+        assert qm.lib().moe_router(router(tokens=0), None, P + off, 0, None) == OK, off
