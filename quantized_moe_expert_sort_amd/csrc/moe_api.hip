@@ -302,7 +302,7 @@ moe_status_t check_norm(const moe_block_norm_t* p, moe::NormArgs* a) {
   if (p->dim > MOE_NORM_MAX_DIM) return MOE_ERR_UNSUPPORTED;
   if (p->tokens > 0 && !p->x) return MOE_ERR_INVALID_ARG;
   *a = moe::NormArgs{p->x, p->y, p->w_post, p->gate, p->w_pre, p->h, p->n, p->q, p->q_scale, p->rstd,
-                     p->tokens, p->dim, p->x_dt, p->gate_kind, p->gate_act, p->q_dt, p->scale, p->eps};
+                     p->rstd ? p->rstd + p->tokens : nullptr, p->tokens, p->dim, p->x_dt, p->gate_kind, p->gate_act, p->q_dt, p->scale, p->eps};
   return MOE_OK;
 }
 

@@ -494,7 +494,11 @@ void run(const Gemm& p, int blocks_k, hipStream_t s) {
 hipError_t launch_quant_i8(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q, float* scale, hipStream_t s) {
   int64_t waves = (cols + 511) / 512;
   if (waves > 16) waves = 16;
-  quant_i8_kernel<<<(unsigned)rows, (unsigned)waves * 64, 0, s>>>(x, (int)cols, q, scale);
+  const int64_t slice = MAX_ITEMS / (waves * 64);
+  for (int64_t r = 0; r < rows; r += slice) {
+    const int64_t n = rows - r < slice ? rows - r : slice;
+    quant_i8_kernel<<<(unsigned)n, (unsigned)waves * 64, 0, s>>>(x + r * cols, (int)cols, q + r * cols, scale + r);
+  }
   return hipGetLastError();
 }
 

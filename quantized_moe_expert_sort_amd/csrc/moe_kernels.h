@@ -133,7 +133,8 @@ struct NormArgs {
   uint16_t* n;             // [T, D] bf16 or null
   void* q;                 // codes or null
   void* q_scale;
-  float* rstd;             // [2, T] or null
+  float* rstd_y;           // [T] 1/rms(y), or null
+  float* rstd_h;           // [T] 1/rms(h), or null
   int T, D, x_dt, gate_kind, gate_act, q_dt;
   float scale, eps;
 };

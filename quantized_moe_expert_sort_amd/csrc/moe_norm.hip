@@ -240,7 +240,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
     if (a.w_post) {
       row_sums<1>(s, red[0], W);
       ry = rsqrt_f(s[0] * inv_d + a.eps);
-      if (a.rstd && tr == 0) a.rstd[row] = ry;
+      if (a.rstd_y && tr == 0) a.rstd_y[row] = ry;
     }
     const float row_gate = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
     const float k = a.scale * ry;
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const NormArgs a, int W) {
     for (int j = 0; j < VEC; ++j) s[0] += h[c][j] * h[c][j];
   row_sums<1>(s, red[1], W);
   const float rh = rsqrt_f(s[0] * inv_d + a.eps);
-  if (a.rstd && tr == 0) a.rstd[a.T + row] = rh;
+  if (a.rstd_h && tr == 0) a.rstd_h[row] = rh;
   uint32_t amax = 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -382,8 +382,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     // opaque, so that the compiler keeps one 32-bit offset instead of a 64-bit address per array and chunk
     int lane_at = tr * VEC;
     asm volatile("" : "+v"(lane_at));
-    const float ry = post ? a.rstd[row] : 1.0f;
-    const float rh = has_dn ? a.rstd[a.T + row] : 0.0f;
+    const float ry = post ? a.rstd_y[row] : 1.0f;
+    const float rh = has_dn ? a.rstd_h[row] : 0.0f;
     const float row_gate = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
     float h[CH][VEC], y[CH][VEC], u[CH][VEC], e[CH][VEC];
     // as in the forward pass: loads without branches on the lane, all in flight together; lanes past
@@ -610,14 +610,36 @@ void norm_dispatch(const NormArgs& a, const Shape& sh, const F& f) {
   else norm_typed<8, 2>(a, f);
 }
 
+// The forward call's rows t .. t + n - 1.
+NormArgs rows_from(const NormArgs& a, int64_t t, int64_t n) {
+  const auto bytes = [](auto* p, int64_t off) { return p ? (decltype(p))((const uint8_t*)p + off) : p; };
+  const int64_t at = t * a.D;
+  NormArgs r = a;
+  r.T = (int)n;
+  r.x = bytes(a.x, at * (a.x_dt == MOE_DT_F32 ? 4 : 2));
+  r.h = bytes(a.h, at * (a.x_dt == MOE_DT_F32 ? 4 : 2));
+  r.y = bytes(a.y, at * 2);
+  r.n = bytes(a.n, at * 2);
+  r.gate = bytes(a.gate, a.gate_kind == MOE_GATE_TOKEN ? t * 4 : a.gate_kind == MOE_GATE_ELEMENT ? at * 2 : 0);
+  r.q = bytes(a.q, a.q_dt == MOE_DT_FP4_E2M1 ? at / 2 : at);
+  r.q_scale = bytes(a.q_scale, a.q_dt == MOE_DT_I8 ? t * 4 : at / 32);
+  r.rstd_y = bytes(a.rstd_y, t * 4);
+  r.rstd_h = bytes(a.rstd_h, t * 4);
+  return r;
+}
+
 }  // namespace
 
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   const Shape sh = norm_shape(a.D);
-  const unsigned grid = (unsigned)((a.T + sh.R - 1) / sh.R);
-  norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto is_short, auto xt) {
-    norm_kernel<vec(), ch(), gate(), is_short(), decltype(xt)><<<grid, sh.threads, 0, s>>>(a, sh.W);
-  });
+  const int64_t slice = MAX_ITEMS / (64 * sh.W);
+  for (int64_t t = 0; t < a.T; t += slice) {
+    const NormArgs part = rows_from(a, t, a.T - t < slice ? a.T - t : slice);
+    const unsigned grid = (unsigned)((part.T + sh.R - 1) / sh.R);
+    norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto is_short, auto xt) {
+      norm_kernel<vec(), ch(), gate(), is_short(), decltype(xt)><<<grid, sh.threads, 0, s>>>(part, sh.W);
+    });
+  }
   return hipGetLastError();
 }
 

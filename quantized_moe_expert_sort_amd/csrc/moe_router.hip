@@ -770,11 +770,25 @@ bool wide_rows(int E, const void* p, const void* q) {
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
 int forward_rows(const RouterArgs& a, void* ws, hipStream_t s) {
   constexpr int waves = router_waves<NREG, BIAS, BAL>();
-  int grid = (a.T + waves - 1) / waves;
-  if (BAL) grid = grid < 1 ? 1 : grid < MOE_ROUTER_PARTS ? grid : MOE_ROUTER_PARTS;
   const size_t lds = waves * CAND * sizeof(uint2) + (BAL ? (size_t)(1 + HAND) * a.E * 4 + 256 : 0);
-  router_kernel<LT, VEC, NREG, BIAS, BAL><<<(unsigned)grid, waves * 64, lds, s>>>(a, ws);
-  return grid;
+  if constexpr (BAL) {
+    const int64_t groups = ((int64_t)a.T + waves - 1) / waves;
+    const int grid = (int)(groups < 1 ? 1 : groups < MOE_ROUTER_PARTS ? groups : MOE_ROUTER_PARTS);
+    router_kernel<LT, VEC, NREG, BIAS, BAL><<<(unsigned)grid, waves * 64, lds, s>>>(a, ws);
+    return grid;
+  } else {
+    RouterArgs part = a;
+    constexpr int64_t slice = MAX_ITEMS / 64;                 // a wave per row; keeps the alignment of the rows
+    for (int64_t t = 0; t < a.T; t += slice) {
+      part.T = (int)(a.T - t < slice ? a.T - t : slice);
+      part.logits = static_cast<const LT*>(a.logits) + t * a.E;
+      part.valid = a.valid ? a.valid + t : nullptr;
+      part.ids = a.ids + t * a.K;
+      part.w = a.w + t * a.K;
+      router_kernel<LT, VEC, NREG, BIAS, BAL><<<(unsigned)((part.T + waves - 1) / waves), waves * 64, lds, s>>>(part, ws);
+    }
+    return 0;
+  }
 }
 // Returns the number of partial sums of the balance statistics.
 template <class LT, int VEC, int NREG>

@@ -6,6 +6,10 @@
 
 namespace moe {
 
+// Work items of a dispatch of whole rows, at most.  A dimension holds fewer than 2^32 of them, and a
+// launch of more runs what is left modulo 2^32, without an error; launchers take their rows in slices.
+constexpr int64_t MAX_ITEMS = (int64_t)1 << 31;
+
 // Lane exchanges on the VALU: quad_perm and the row mirrors inside each row of 16 lanes, then the
 // two row swaps.  Every step combines a lane with one partner that does the same with it, so for a
 // commutative operation all 64 lanes end with the same bits.
