@@ -648,9 +648,9 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& b, hipStream_t s) 
   const Shape sh = norm_shape(a.D);
   // Beyond a row per workgroup, as many rows at a time as 16 waves take: fewer partial sums than
   // with more workgroups of fewer waves (4096 x 3584: 54 us, 60 with 512 workgroups; 9000 x 130: 14, 17)
-  const int want = (a.T + MOE_NORM_PARTS - 1) / MOE_NORM_PARTS, fit = sh.ch * sh.vec > 8 ? 1 : MAX_W / sh.W;
-  const int R = want < fit ? want : fit;
-  const int groups = R > 0 ? (a.T + R - 1) / R : 0;
+  const int64_t want = ((int64_t)a.T + MOE_NORM_PARTS - 1) / MOE_NORM_PARTS;
+  const int fit = sh.ch * sh.vec > 8 ? 1 : MAX_W / sh.W, R = want < fit ? (int)want : fit;
+  const int64_t groups = R > 0 ? ((int64_t)a.T + R - 1) / R : 0;
   const unsigned grid = (unsigned)(groups < MOE_NORM_PARTS ? groups : MOE_NORM_PARTS);
   if (grid > 0) {                                             // no rows: the sums below are zero
     norm_dispatch(a, sh, [&](auto vec, auto ch, auto gate, auto is_short, auto xt) {

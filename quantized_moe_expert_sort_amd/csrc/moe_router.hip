@@ -812,7 +812,7 @@ int forward(const RouterArgs& a, bool bal, void* ws, hipStream_t s) {
 
 template <class LT>
 void backward(const RouterArgs& a, const BalanceArgs& o, const float* dw, const float* dloss, void* dlogits, hipStream_t s) {
-  const unsigned groups = (unsigned)((a.T + 3) / 4);
+  const unsigned groups = (unsigned)(((int64_t)a.T + 3) / 4);
   const unsigned grid = groups < 1024u ? groups : 1024u;
   const size_t lds = (size_t)5 * a.E * 4;
   LT* const d = static_cast<LT*>(dlogits);

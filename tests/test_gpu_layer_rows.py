@@ -69,3 +69,15 @@ def test_quant():
     ql, sl = qm.moe_quant_i8(b)
     same(q, ql, "codes")
     same(s, sl, "scales")
+
+
+def test_block_norm_of_as_many_rows_as_an_int_counts():
+    # rows of one element: 1/rms is 1 (eps is below the last place), so dx = dh, and dw_pre counts the rows
+    n = (1 << 31) - 1
+    x = torch.ones(n, 1, dtype=torch.bfloat16, device="cuda")
+    w = torch.full((1,), 2.0, device="cuda")
+    r = qm.moe_block_norm(x, w_pre=w, eps=1e-12, stats=True)
+    assert all((part == 2).all() for part in r.n.split(1 << 28))
+    b = qm.moe_block_norm_backward(x, None, r.rstd, x, x, w_pre=w)
+    assert all((part == 1).all() for part in b.dx.split(1 << 28))
+    assert float(b.dw_pre) == 2.0 ** 31                        # rounded to fp32
