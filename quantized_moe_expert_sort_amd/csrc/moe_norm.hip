@@ -147,6 +147,23 @@ __device__ __forceinline__ void store_own(T* row, int col, int D, bool split, co
   }
 }
 
+// The sigmoid and its slope.  With p = sigmoid(-|x|) <= 1/2 the slope is p (1 - p) on both sides; from s
+// alone, s (1 - s) loses its digits where s is next to 1 (4e-5 of the slope at x = 8) and is 0 from 17 on.
+__device__ __forceinline__ float sigmoid_slope(float x, float& slope) {
+  const float p = sigmoid_f(-__builtin_fabsf(x));
+  slope = __builtin_fmaf(-p, p, p);
+  return x > 0.0f ? 1.0f - p : p;
+}
+// Both in one register: p with the sign of -x, and from it the slope and, with one = 1, the sigmoid.
+__device__ __forceinline__ float signed_sigmoid(float x) {
+  return __builtin_copysignf(sigmoid_f(-__builtin_fabsf(x)), -x);
+}
+__device__ __forceinline__ float signed_slope(float c) {
+  const float p = __builtin_fabsf(c);
+  return __builtin_fmaf(-p, p, p);
+}
+__device__ __forceinline__ float signed_value(float c, float one) { return c + (__float_as_int(c) < 0 ? one : 0.0f); }
+
 // The gate of this lane's VEC elements after its activation (GATE: what it is shared by), from what
 // was loaded for them.  row_gate: the row's gate with MOE_GATE_TOKEN.
 template <int GATE, int VEC>
@@ -331,6 +348,11 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, has_dn = b.dn != nullptr, has_dh = b.dh != nullptr;
   const bool sigmoid = a.gate_act == MOE_GATE_SIGMOID;
   constexpr bool fixed_gate = GATE == MOE_GATE_CHANNEL || GATE == MOE_GATE_NONE;
+  // A sigmoid per element: gate and slope in two registers, or both in one where registers are short
+  // (bf16 4096 x 3584 50 us, 54 in one; 1000 x 12000 in one 74 us with its partial sums, 83 in two)
+  constexpr bool KEEP_SLOPE = GATE == MOE_GATE_ELEMENT && CH * VEC <= 8;
+  constexpr bool IN_ONE = GATE == MOE_GATE_ELEMENT && !KEEP_SLOPE;
+  const float one = sigmoid ? 1.0f : 0.0f;
   const bool split = SHORT && holds_short<VEC, CH>(W, tr, a.D);
   // acc_post: sum of dz yh, or with a gate per channel of scale e yh, which gives both dw_post (times
   // g) and the gate's gradient (times w_post and the activation's slope) after the last row
@@ -374,6 +396,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
       for (int j = 0; j < VEC; ++j) w[j] = reg[c][j];
     }
   };
+  const auto gate_at = [&](int c, int j) { return IN_ONE ? signed_value(g[c][j], one) : g[c][j]; };
   int parity = 0;
   for (int64_t top = (int64_t)blockIdx.x * R; top < a.T; top += (int64_t)gridDim.x * R, parity ^= 1) {
     const bool live = top + sub < a.T;                        // else a turn without a row: zeros, no stores
@@ -385,7 +408,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     const float ry = post ? a.rstd_y[row] : 1.0f;
     const float rh = has_dn ? a.rstd_h[row] : 0.0f;
     const float row_gate = GATE == MOE_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
-    float h[CH][VEC], y[CH][VEC], u[CH][VEC], e[CH][VEC];
+    float h[CH][VEC], y[CH][VEC], u[CH][VEC], e[CH][VEC], slope[KEEP_SLOPE ? CH : 1][VEC];
     // as in the forward pass: loads without branches on the lane, all in flight together; lanes past
     // the row hold zeros in h, y, u and e
 #pragma unroll
@@ -408,7 +431,16 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
         if (has_dh) own_part<VEC>(col, a.D, e[c]);
         if constexpr (GATE == MOE_GATE_ELEMENT) own_part<VEC>(col, a.D, g[c]);
       }
-      if constexpr (!fixed_gate) gate_values<GATE, VEC>(a, row_gate, g[c]);
+      if constexpr (GATE == MOE_GATE_TOKEN) gate_values<GATE, VEC>(a, row_gate, g[c]);
+      if constexpr (GATE == MOE_GATE_ELEMENT) {
+        if (sigmoid) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            if constexpr (KEEP_SLOPE) g[c][j] = sigmoid_slope(g[c][j], slope[c][j]);
+            else g[c][j] = signed_sigmoid(g[c][j]);
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         h[c][j] = out ? 0.0f : h[c][j];
@@ -425,7 +457,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
         float w[VEC];
         weights(w_post, c, at, 0, w);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) h[c][j] += a.scale * g[c][j] * (y[c][j] * w[j]);
+        for (int j = 0; j < VEC; ++j) h[c][j] += a.scale * gate_at(c, j) * (y[c][j] * w[j]);
       }
       if (has_dn) {
         float v[VEC];
@@ -462,14 +494,14 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         const float se = a.scale * e[c][j];
-        const float dz = se * g[c][j];
+        const float dz = se * gate_at(c, j);
         u[c][j] = dz * w[j];
         acc_post[c][j] += (GATE == MOE_GATE_CHANNEL ? se : dz) * y[c][j];
         s2[0] += u[c][j] * y[c][j];
         if constexpr (GATE == MOE_GATE_TOKEN || GATE == MOE_GATE_ELEMENT) {
           dg[j] = se * (y[c][j] * w[j]);
-          if (sigmoid) dg[j] *= g[c][j] * (1.0f - g[c][j]);
           if constexpr (GATE == MOE_GATE_TOKEN) s2[1] += dg[j];
+          else if (sigmoid) dg[j] *= KEEP_SLOPE ? slope[c][j] : signed_slope(g[c][j]);
         }
       }
       if constexpr (GATE == MOE_GATE_ELEMENT)
@@ -477,6 +509,11 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     }
     if constexpr (GATE == MOE_GATE_TOKEN) {
       row_sums<2>(s2, red[parity][1], W, first);
+      if (sigmoid) {
+        float k;
+        sigmoid_slope(row_gate, k);
+        s2[1] *= k;
+      }
       if (live && tr == 0) static_cast<float*>(b.dgate)[row] = s2[1];
     } else if (post) {
       row_sums<1>(reinterpret_cast<float(&)[1]>(s2), red[parity][1], W, first);
@@ -532,11 +569,22 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(const NormBackwardA
     float dg[CH][VEC];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
+      const int col = (c * W * 64 + tr) * VEC;
       float w[VEC];
-      weights(w_post, c, (c * W * 64 + tr) * VEC, 0, w);
+      weights(w_post, c, col, 0, w);
+      if (sigmoid) {
+        float raw[VEC];
+        load_own<VEC>(static_cast<const float*>(a.gate), col, a.D, split, raw);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          float k;
+          sigmoid_slope(raw[j], k);
+          w[j] *= k;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        dg[c][j] = acc_post[c][j] * (sigmoid ? w[j] * g[c][j] * (1.0f - g[c][j]) : w[j]);
+        dg[c][j] = acc_post[c][j] * w[j];
         acc_post[c][j] *= g[c][j];
       }
     }
