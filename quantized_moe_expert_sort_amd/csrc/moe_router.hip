@@ -577,7 +577,7 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(const RouterArgs a
 
 // d_logits of one row per wave.  With t_k the gradient that reaches the chosen expert k through
 // its weight (times ds/dl), a_i = d_loss[0] coef c_i E / (K Tv^2):
-//   softmax: dl_i = t_i - p_i sum t + p_i (a_i - sum a p);  sigmoid: t_i + p_i (1 - s_i) (a_i - sum a p)
+//   softmax: dl_i = t_i - p_i sum t + p_i (a_i - sum a p);  sigmoid: t_i + p_i s(-l_i) (a_i - sum a p)
 // plus d_loss[1] z_coef 2 lse / Tv softmax(l)_i.  t is spread over the row through LDS; an expert
 // that the ids name twice gets the sum.
 template <class LT, int VEC, int NREG>
@@ -671,7 +671,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
           tk = v * g;
           tsum = softmax ? wave_sum(tk) : 0.0f;
         }
-        if (!softmax) tk *= 1.0f - v;
+        if (!softmax) tk *= fast_sigmoid(-lk);                // 1 - v would cancel
         if (id >= 0) atomicAdd(&t_row[id], tk);
         wave_sync();
       }
@@ -726,7 +726,7 @@ __global__ __launch_bounds__(256) void router_backward_kernel(const RouterArgs a
           for (int j = 0; j < VEC; ++j) {
             const int i = c * VEC + j;
             float d = 0.0f;
-            if (o.counts) d = ex[i] * (1.0f - fast_sigmoid(l[i])) * (v[j] - mean) * inv_s;
+            if (o.counts) d = ex[i] * fast_sigmoid(-l[i]) * (v[j] - mean) * inv_s;
             if (kz != 0.0f) d += kz * exp_f(l[i] - m);
             l[i] = d;
           }

@@ -51,3 +51,37 @@ def test_block_norm(kind, T, D, x_dt):
     for k in ("dx", "dy", "dw_post", "dw_pre"):
         got = getattr(b, k)
         within(got, want[k], 3 * m[k], 64 * ref.HALF_F32 + ref.half_step(got.dtype))
+
+
+@pytest.mark.parametrize("E,K", [(24, 4), (257, 8), (896, 16), (1100, 8)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_router_sigmoid_scores(E, K, renorm):
+    # rows from wholly saturated to mixed; REL as in the router's tests
+    T, rel = 24, 128 * ref.HALF_F32
+    logits = spread_points((T, E), E)
+    logits[:4] = logits[:4].abs().clamp(min=8.0) + 0.001 * torch.arange(E)
+    g = torch.Generator().manual_seed(E)
+    dw = torch.randn(T, K, generator=g)
+    kw = dict(score="sigmoid", renorm=renorm, scale=1.5)
+    r = qm.moe_router(logits.cuda(), K, balance=(0.4, 0.0), **kw)
+    ids = r.ids.cpu().long()
+    l = logits.double()
+    s, rest = torch.sigmoid(l), torch.sigmoid(-l)
+    # the weights' part
+    sk, gk = s.gather(1, ids), dw.double()
+    v = sk / sk.sum(1, keepdim=True) if renorm else sk
+    mean = (v * gk).sum(1, keepdim=True) if renorm else torch.zeros(T, 1, dtype=torch.float64)
+    size = (v * gk.abs()).sum(1, keepdim=True) if renorm else torch.zeros(T, 1, dtype=torch.float64)
+    own = torch.zeros(T, E, dtype=torch.float64).scatter(1, ids, 1.5 * v * (gk - mean)) * rest
+    own_m = torch.zeros(T, E, dtype=torch.float64).scatter(1, ids, 1.5 * v * (gk.abs() + size)) * rest
+    got = qm.moe_router_backward(logits.cuda(), r._replace(balance=None), dw.cuda(), **kw)
+    bad = (ref.f64(got) - own).abs() > rel * own_m + ref.HALF_F32 * own.abs()
+    assert not bad.any(), (int(bad.sum()), l[bad][:8].tolist())
+    # and the balance loss's, with a gradient of 2 for it
+    a = 2.0 * 0.4 * torch.bincount(ids.flatten(), minlength=E) * E / (K * T * T)
+    p = s / s.sum(1, keepdim=True)
+    am = (a * p).sum(1, keepdim=True)
+    want, m = own + p * rest * (a - am), own_m + p * rest * (a + am)
+    got = qm.moe_router_backward(logits.cuda(), r, dw.cuda(), d_loss=torch.tensor([2.0, 0.0]).cuda(), **kw)
+    bad = (ref.f64(got) - want).abs() > 2 * rel * m + ref.HALF_F32 * want.abs()
+    assert not bad.any(), (int(bad.sum()), l[bad][:8].tolist())
