@@ -36,6 +36,7 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float BIG = 3.402823466e38f;
 constexpr int CAND = 64;                      // candidates of a row, at most one per lane
 constexpr int HAND = 4;                       // rows of LDS in which waves hand over their sums
+constexpr int TURNS = 64;                     // rows that a wave adds up in fp32
 
 // LDS written by some lanes of a wave is read by others of the same wave after this.
 __device__ __forceinline__ void wave_sync() {
@@ -395,9 +396,11 @@ constexpr int router_waves() { return !BAL ? 4 : BIAS || NREG > 16 ? 8 : 16; }
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
 __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router_kernel(const RouterArgs a, void* ws) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int lane0 = threadIdx.x & 63, lane = lane0, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   uint2* const cand = reinterpret_cast<uint2*>(lds) + wave * CAND;
-  int32_t* const hist = reinterpret_cast<int32_t*>(lds + (size_t)waves * CAND * sizeof(uint2));   // BAL: [E]
+  double* const zsums = reinterpret_cast<double*>(lds + (size_t)waves * CAND * sizeof(uint2));    // BAL: [waves]
+  double* const total = zsums + waves;                                                            // BAL: [E]
+  int32_t* const hist = reinterpret_cast<int32_t*>(total + a.E);                                  // BAL: [E]
   float* const handed = reinterpret_cast<float*>(hist + a.E);                                     // BAL: [HAND, E]
   float psum[BAL ? NREG : 1];
   float zsum = 0.0f;
@@ -413,8 +416,12 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
   int64_t t = (int64_t)blockIdx.x * waves + wave;
   Row<LT, VEC, NREG> ahead;
   if (t < a.T) ahead.load(static_cast<const LT*>(a.logits) + t * a.E, a.E, lane);
-  for (; t < a.T; t += step) {
+  const auto take = [&](const int64_t t) {
     const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
+    // opaque where it is short of registers: the columns' addresses and masks would be kept over the rows
+    // and spill (3040 x 1177 with a bias 26 us, 41 with them kept)
+    int lane = lane0;
+    if constexpr ((BIAS || BAL) && NREG > (VEC == 1 ? 4 : 16)) asm volatile("" : "+v"(lane));
     int id = -1;
     float w = 0.0f;
     float l[NREG];
@@ -467,10 +474,62 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
       a.ids[t * a.K + lane] = id;
       a.w[t * a.K + lane] = w;
     }
-  }
-  if constexpr (BAL) {
+  };
+  if constexpr (!BAL) {
+    for (; t < a.T; t += step) take(t);
+  } else {
+    // The waves' probability sums of TURNS rows each, HAND waves at a time through LDS; each thread adds
+    // its columns in the order of the waves.  Where a wave has more rows, these sums are added in 64 bits:
+    // the rounding of the statistics does not grow with the number of rows.
+    constexpr int COLS = (64 * NREG + 64 * router_waves<NREG, BIAS, BAL>() - 1) / (64 * router_waves<NREG, BIAS, BAL>());
+    const int64_t top = (int64_t)blockIdx.x * waves;
+    float sum[COLS];
+    for (int64_t from = top;; from += TURNS * step) {
+      const int64_t end = min((int64_t)a.T, t + TURNS * step);
+      for (; t < end; t += step) take(t);
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) sum[c] = 0.0f;
+      int me = threadIdx.x;                                   // opaque: addresses kept over the rows would spill
+      asm volatile("" : "+v"(me));
+      for (int base = 0; base < waves; base += HAND) {
+        __syncthreads();
+        if (wave >= base && wave < base + HAND) {
+#pragma unroll
+          for (int c = 0; c < NREG / VEC; ++c) {
+            const int col = (c * 64 + (me & 63)) * VEC;
+            float v[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) { v[j] = psum[c * VEC + j]; psum[c * VEC + j] = 0.0f; }
+            if (col < a.E) store_row<VEC>(handed + (wave - base) * a.E + col, v);
+          }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) {
+          const int col = min(c * (int)blockDim.x + me, a.E - 1);
+#pragma unroll
+          for (int k = 0; k < HAND; ++k) sum[c] += handed[k * a.E + col];
+        }
+      }
+      const bool first = from == top, last = from + TURNS * step >= a.T;   // the same for every wave
+      if (first && last) break;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const int col = c * (int)blockDim.x + me;
+        if (col < a.E) {
+          total[col] = (first ? 0.0 : total[col]) + sum[c];
+          sum[c] = (float)total[col];
+        }
+      }
+      if (lane == 0) zsums[wave] = (first ? 0.0 : zsums[wave]) + zsum;
+      zsum = 0.0f;
+      if (last) {
+        if (lane == 0) zsum = (float)zsums[wave];
+        break;
+      }
+    }
     const BalanceParts b = balance_parts(ws, a.E);
-    int* const small = reinterpret_cast<int*>(handed);        // tv and z of each wave first
+    int* const small = reinterpret_cast<int*>(handed);        // tv and z of each wave
     __syncthreads();
     if (lane == 0) { small[2 * wave] = tv; small[2 * wave + 1] = __float_as_int(zsum); }
     __syncthreads();
@@ -482,30 +541,6 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
       b.z[blockIdx.x] = q;
     }
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) b.counts[(int64_t)blockIdx.x * a.E + e] = hist[e];
-    // the waves' probability sums, HAND waves at a time through LDS; each thread adds its columns in
-    // the order of the waves
-    constexpr int COLS = (64 * NREG + 64 * router_waves<NREG, BIAS, BAL>() - 1) / (64 * router_waves<NREG, BIAS, BAL>());
-    float sum[COLS] = {};
-    for (int base = 0; base < waves; base += HAND) {
-      __syncthreads();
-      if (wave >= base && wave < base + HAND) {
-#pragma unroll
-        for (int c = 0; c < NREG / VEC; ++c) {
-          const int col = (c * 64 + lane) * VEC;
-          float v[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] = psum[c * VEC + j];
-          if (col < a.E) store_row<VEC>(handed + (wave - base) * a.E + col, v);
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int c = 0; c < COLS; ++c) {
-        const int col = min(c * (int)blockDim.x + (int)threadIdx.x, a.E - 1);
-#pragma unroll
-        for (int k = 0; k < HAND; ++k) sum[c] += handed[k * a.E + col];
-      }
-    }
 #pragma unroll
     for (int c = 0; c < COLS; ++c) {
       const int col = c * blockDim.x + threadIdx.x;
@@ -770,7 +805,7 @@ bool wide_rows(int E, const void* p, const void* q) {
 template <class LT, int VEC, int NREG, bool BIAS, bool BAL>
 int forward_rows(const RouterArgs& a, void* ws, hipStream_t s) {
   constexpr int waves = router_waves<NREG, BIAS, BAL>();
-  const size_t lds = waves * CAND * sizeof(uint2) + (BAL ? (size_t)(1 + HAND) * a.E * 4 + 256 : 0);
+  const size_t lds = waves * CAND * sizeof(uint2) + (BAL ? waves * 8 + (size_t)(3 + HAND) * a.E * 4 + 256 : 0);
   if constexpr (BAL) {
     const int64_t groups = ((int64_t)a.T + waves - 1) / waves;
     const int grid = (int)(groups < 1 ? 1 : groups < MOE_ROUTER_PARTS ? groups : MOE_ROUTER_PARTS);

@@ -4,6 +4,7 @@ not zero."""
 import pytest
 import torch
 
+import _layer_ref as ref
 import quantized_moe_expert_sort_amd as qm
 
 pytestmark = pytest.mark.gpu
@@ -79,3 +80,25 @@ def test_quant():
     ql, sl = qm.moe_quant_i8(last)
     assert torch.equal(q[-ROWS:], ql) and torch.equal(s[-ROWS:], sl)
     assert not q[:-ROWS].any() and not s[:-ROWS].any()
+
+
+@pytest.mark.parametrize("E,score,dt", [(7, "softmax", torch.bfloat16), (11, "sigmoid", torch.float32), (1030, "softmax", torch.bfloat16),
+                                        (512, "softmax", torch.float32), (1024, "sigmoid", torch.bfloat16)])
+def test_statistics_of_many_rows(E, score, dt):
+    # rows that are all alike round alike: a chain of fp32 sums over all rows of a wave would be off by
+    # up to the number of rows in it times 2^-24.  The bound is the same as for a short batch.
+    T, K = min((1 << 24) + 77, (1 << 31) // E - 1), 3
+    row = torch.linspace(-1.0, 1.0, E).to(dt)
+    logits = row.cuda().expand(T, E).contiguous()
+    r = qm.moe_router(logits, K, score=score, balance=(0.3, 0.02))
+    l = row.double()
+    p = torch.softmax(l if score == "softmax" else torch.nn.functional.logsigmoid(l), 0)
+    rel = 128 * 2.0 ** -24                                     # as in the router's tests
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts[ref.router_choice(row[None], K, score)[0].long()] = T
+    assert torch.equal(r.balance.counts.cpu().long(), counts) and int(r.balance.num_valid) == T
+    off = ((ref.f64(r.balance.mean_prob) - p).abs() / p).max()
+    assert off <= 2 * rel, float(off / rel)
+    want = torch.stack((0.3 * (counts * (E / (K * T)) * p).sum(), 0.02 * torch.logsumexp(l, 0).square()))
+    off = ((ref.f64(r.balance.loss) - want).abs() / want).max()
+    assert off <= 4 * rel, float(off / rel)
