@@ -102,3 +102,23 @@ def test_statistics_of_many_rows(E, score, dt):
     want = torch.stack((0.3 * (counts * (E / (K * T)) * p).sum(), 0.02 * torch.logsumexp(l, 0).square()))
     off = ((ref.f64(r.balance.loss) - want).abs() / want).max()
     assert off <= 4 * rel, float(off / rel)
+
+
+@pytest.mark.parametrize("T,D,dt", [((1 << 24) + 77, 8, torch.bfloat16), (2_000_003, 600, torch.float32), (300_007, 8200, torch.bfloat16)])
+def test_weight_gradients_of_many_rows(T, D, dt):
+    # as above: alike rows round alike, and the bound (that of the norm's tests) does not grow with them
+    g = torch.Generator().manual_seed(D)
+    x, dh = (torch.randn(1, D, generator=g).to(dt) for _ in range(2))
+    y, dn = (torch.randn(1, D, generator=g).to(torch.bfloat16) for _ in range(2))
+    w, v, gate = 1 + 0.3 * torch.randn(D, generator=g), 1 + 0.3 * torch.randn(D, generator=g), torch.randn(D, generator=g)
+    kw = dict(w_post=w.cuda(), w_pre=v.cuda(), gate=gate.cuda(), gate_kind="channel", gate_act="sigmoid", scale=0.7)
+    xs, ys, dhs, dns = (t.cuda().expand(T, D).contiguous() for t in (x, y, dh, dn))
+    rstd = torch.empty(2, T, device="cuda")
+    rstd.copy_(qm.moe_block_norm(x.cuda(), y.cuda(), eps=1e-5, stats=True, **kw).rstd.expand(2, T))
+    b = qm.moe_block_norm_backward(xs, ys, rstd, dhs, dns, **kw)
+    want, m = ref.norm_backward(*(t.double() for t in (x, y, w, gate)), "channel", "sigmoid", 0.7, v.double(), 1e-5, dh.double(), dn.double())
+    for k in ("dw_post", "dw_pre", "dgate"):
+        off = (ref.f64(getattr(b, k)) - T * want[k]).abs() / (T * (3 * 64 * 2.0 ** -24 * m[k] + 2.0 ** -24 * want[k].abs()))
+        assert off.max() <= 1, (k, float(off.max()))
+    for k in ("dx", "dy"):
+        assert (getattr(b, k) == getattr(b, k)[:1]).all(), k
