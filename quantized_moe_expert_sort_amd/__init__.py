@@ -385,6 +385,12 @@ def _need(t, name, dtype, shape, index):
                      f"{'a dense' if t.is_contiguous() else 'a strided'} {t.dtype} of {tuple(t.shape)} on {t.device}")
 
 
+def _sizes(*values):
+    """Refuses sizes that the library's 32-bit arguments cannot hold (ctypes would wrap them)."""
+    if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
+        raise ValueError(f"sizes have to fit 32 bits, got {', '.join(map(str, values))}")
+
+
 def _pick(table, key, name):
     if key not in table:
         raise ValueError(f"{name}: {key!r} is none of {', '.join(table)}")
@@ -420,6 +426,7 @@ def _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, eps, ind
     if x.dim() != 2 or x.dtype not in _ROW_TYPES:
         raise ValueError(f"x: need a bfloat16 or float32 tensor [tokens, dim], got {x.dtype} of {tuple(x.shape)}")
     T, D = x.shape
+    _sizes(T, D)
     kind = _pick(GATES, gate_kind, "gate_kind")
     if (gate is None) != (kind == 0):
         raise ValueError("gate and gate_kind go together")
@@ -508,6 +515,7 @@ def _router_params(logits, topk, score, renorm, scale, bias, valid, index):
         raise ValueError(f"logits: need a bfloat16 or float32 tensor [tokens, experts], got {logits.dtype} of "
                          f"{tuple(logits.shape)}")
     T, E = logits.shape
+    _sizes(T, E, topk)
     if valid is not None and valid.dtype == torch.bool:
         valid = valid.view(torch.uint8)
     r = RouterParams(tokens=T, num_experts=E, topk=topk, dt=_ROW_TYPES[logits.dtype],
@@ -591,6 +599,7 @@ def moe_pack_i8(w, out=None):
     if w.dim() != 2:
         raise ValueError(f"w: need [out_features, in_features], got {tuple(w.shape)}")
     N, K = w.shape
+    _sizes(N, K)
     shape = i8_packed_shape(N, K)
     if out is None:
         out = torch.empty(shape, dtype=torch.int8, device=device)
@@ -609,6 +618,7 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
                          f"{tuple(w_scale.shape)}")
     T, K = a.shape
     N = w_scale.shape[0]
+    _sizes(T, N, K)
     params = None
     if act is not None:
         k = _pick(ACTS, act, "act")

@@ -210,3 +210,34 @@ def test_workspaces_have_to_be_aligned_like_their_words():
         assert backward_status(ws=P + off) == INVALID, off
         # where no workspace is read, its address does not matter
         assert qm.lib().moe_router(router(tokens=0), None, P + off, 0, None) == OK, off
+
+
+def test_binding_refuses_sizes_that_its_32_bit_fields_would_wrap(monkeypatch):
+    # 2^32 + 5 rows would arrive as 5; tensors without storage stand for ones of that size
+    def reached(fn, *args):
+        raise AssertionError(f"{fn} was called")
+    monkeypatch.setattr(qm, "_on_gpu", lambda t, name: (t.device, t.get_device()))
+    monkeypatch.setattr(qm, "_call", reached)
+    big = (1 << 32) + 16
+
+    def empty(*shape, dtype=torch.bfloat16):
+        return torch.empty(*shape, dtype=dtype, device="meta")
+    i8, f32, i32 = torch.int8, torch.float32, torch.int32
+    w = empty(1, dtype=f32)
+    ids = empty(big, 1, dtype=i32)
+    packed = empty(*qm.i8_packed_shape(16, 16), dtype=i8)
+    for call in (lambda: qm.moe_block_norm(empty(big, 1), w_pre=w, want_n=False, h=empty(big, 1)),
+                 lambda: qm.moe_block_norm(empty(1, big), h=empty(1, big)),
+                 lambda: qm.moe_block_norm_backward(empty(big, 1), None, empty(2, big, dtype=f32), None, empty(big, 1), w_pre=w),
+                 lambda: qm.moe_router(empty(big, 1), 1),
+                 lambda: qm.moe_router(empty(1, big), 1),
+                 lambda: qm.moe_router(empty(0, 8), big),
+                 lambda: qm.moe_router(empty(1, 8), 2 - (1 << 32)),
+                 lambda: qm.moe_router_backward(empty(big, 1), qm.Routing(ids, None, None), empty(big, 1, dtype=f32)),
+                 lambda: qm.moe_pack_i8(empty(big, 16, dtype=i8)),
+                 lambda: qm.moe_pack_i8(empty(16, big, dtype=i8)),
+                 lambda: qm.moe_gemm_i8(empty(big, 16, dtype=i8), empty(big, dtype=f32), packed, empty(16, dtype=f32)),
+                 lambda: qm.moe_gemm_i8(empty(1, big, dtype=i8), empty(1, dtype=f32), packed, empty(16, dtype=f32)),
+                 lambda: qm.moe_gemm_i8(empty(1, 16, dtype=i8), empty(1, dtype=f32), packed, empty(big, dtype=f32))):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
