@@ -5,6 +5,7 @@ import ctypes
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -241,3 +242,24 @@ def test_binding_refuses_sizes_that_its_32_bit_fields_would_wrap(monkeypatch):
                  lambda: qm.moe_gemm_i8(empty(1, 16, dtype=i8), empty(1, dtype=f32), packed, empty(big, dtype=f32))):
         with pytest.raises(ValueError, match="32 bits"):
             call()
+
+
+def test_import_needs_nothing_of_torch_beyond_its_public_names():
+    # a build of torch without the private getters of device and stream: the package imports, and calls
+    # take both from torch.cuda
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import quantized_moe_expert_sort_amd as qm
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_device = lambda: 3
+torch.cuda.current_stream = lambda index: Stream
+assert qm._current_device() == 3 and qm._raw_stream(3) == 77
+assert not torch.cuda.is_initialized()
+print("imported")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0 and "imported" in r.stdout, r.stderr[-2000:]
