@@ -103,8 +103,26 @@ struct Gemm {
   float beta, inv_beta, lb, inv_lb;
 };
 
+// 1 - 2^s for s <= 0.  Near 0 the difference would keep only what 2^s holds beside 1 (1% at s = -1e-5); there
+// the first two terms of its series, off by s^2 / 12.5 < 2^-17 of it, beyond them 2^-24 of at least 2^-7.5.
+__device__ __forceinline__ float one_minus_exp2(float s) {
+  constexpr float LN2 = 0.6931471805599453f;
+  const float near = s * __builtin_fmaf(s, -0.5f * LN2 * LN2, -LN2);
+  return s > -0x1p-7f ? near : 1.0f - __builtin_amdgcn_exp2f(s);
+}
+// As situv2, with each tanh to a bf16's last place however small its argument.
+__device__ __forceinline__ float situv2_small(float g, float u, const Gemm& p) {
+  constexpr float LOG2E = 1.4426950408889634f;
+  const float ag = __builtin_fabsf(g), au = __builtin_fabsf(u);
+  const float a = one_minus_exp2(ag * (-2.0f * LOG2E * p.inv_beta));
+  const float b = __builtin_amdgcn_exp2f(ag * -LOG2E);
+  const float c = one_minus_exp2(au * (-2.0f * LOG2E * p.inv_lb));
+  const float d = 2.0f - a, den = __builtin_fmaf(d, b, d) * (2.0f - c);
+  const float y = (p.beta * p.lb) * (a * c * (g < 0.0f ? b : 1.0f)) * __builtin_amdgcn_rcpf(den);
+  return __builtin_copysignf(y, __uint_as_float(__float_as_uint(g) ^ __float_as_uint(u)));
+}
 __device__ __forceinline__ float activate(const Gemm& p, float g, float u) {
-  return p.act == MOE_ACT_SITUV2 ? situv2(g, u, p.beta, p.inv_beta, p.lb, p.inv_lb) : silu_mul(g, u);
+  return p.act == MOE_ACT_SITUV2 ? situv2_small(g, u, p) : silu_mul(g, u);
 }
 
 // One output, channel c of token t.
@@ -364,6 +382,13 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
 #pragma unroll
   for (int n = 0; n < FO; ++n) {
     const int cw = c0 + wn * (FO * 32) + n * 32;              // first channel of the group
+    float sw[16], sw_up[ACT ? 16 : 1];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = min(cw + 8 * (i / 4) + 4 * hl + i % 4, p.No - 1);
+      sw[i] = p.sw[c];
+      if constexpr (ACT) sw_up[i] = p.sw[p.No + c];
+    }
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
       const int64_t t = t0 + wm * WM + m * 32 + (lane & 31);
@@ -371,9 +396,8 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const int c = min(cw + 8 * (i / 4) + 4 * hl + i % 4, p.No - 1);
-        v[i] = (float)acc[n][m][i] * (sa * p.sw[c]);
-        if constexpr (ACT) v[i] = activate(p, v[i], (float)acc[n + FO][m][i] * (sa * p.sw[p.No + c]));
+        v[i] = (float)acc[n][m][i] * (sa * sw[i]);
+        if constexpr (ACT) v[i] = activate(p, v[i], (float)acc[n + FO][m][i] * (sa * sw_up[i]));
       }
       // halves of two 8-channel groups exchanged: lanes 0..31 hold the first, 32..63 the second
 #pragma unroll

@@ -164,3 +164,25 @@ def test_quant_edges():
     assert torch.equal(q.cpu()[keep], wq) and torch.equal(s.cpu()[keep], ws)
     assert torch.isnan(s[[4, 5]]).all() and (q[[4, 5]] == 0).all()
     assert (q[[0, 1]] == 0).all() and (s[[0, 1]] == 0).all()
+
+
+@pytest.mark.parametrize("T", [3, 40, 700])
+@pytest.mark.parametrize("small", ["gate", "up", "both"])
+def test_situv2_of_small_values(T, small):
+    # tanh(x) near 0 is x: a quotient through 1 - exp(-2x) would lose what exp rounds away, 1% at x = 5e-6.
+    # Besides the rounding to bf16 each tanh may be off by 2^-15 of itself (its worst is where the
+    # exponential takes over: a last place of 2^-24 beside 1 - exp = 2^-7.5), the scales' products and the
+    # rest by 32 roundings of fp32.
+    N, K = 256, 16
+    g = torch.Generator().manual_seed(T)
+    size = lambda n, on: torch.exp2(-24 * torch.rand(n, generator=g)) if on else 0.5 + torch.rand(n, generator=g)   # noqa: E731
+    sw = torch.cat((size(N // 2, small != "up"), size(N // 2, small != "gate")))
+    a = torch.randint(-127, 128, (T, K), generator=g, dtype=torch.int32).to(torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int32).to(torch.int8)
+    sa = (0.5 + torch.rand(T, generator=g)) / 127 ** 2
+    out = qm.moe_gemm_i8(a.cuda(), sa.cuda(), qm.moe_pack_i8(w.cuda()), sw.cuda(), act="situv2", beta=4.0, linear_beta=25.0)
+    r = (ref.f64(a) @ ref.f64(w).t()) * ref.f64(sa)[:, None] * ref.f64(sw)
+    gate, up = r[:, :N // 2], r[:, N // 2:]
+    want = 4.0 * torch.tanh(gate / 4.0) * torch.sigmoid(gate) * 25.0 * torch.tanh(up / 25.0)
+    bad = (ref.f64(out) - want).abs() > (ref.HALF_BF16 + 2 * 2.0 ** -15 + 32 * ref.HALF_F32 * (1 + gate.abs())) * want.abs()
+    assert not bad.any(), (int(bad.sum()), gate[bad][:4].tolist(), up[bad][:4].tolist())
