@@ -488,9 +488,10 @@ def moe_block_norm(x, y=None, *, w_post=None, gate=None, gate_kind="none", gate_
 
 
 def moe_block_norm_backward(x, y, rstd, dh, dn, *, w_post=None, gate=None, gate_kind="none", gate_act="none",
-                            scale=1.0, w_pre=None, ws=None):
+                            scale=1.0, w_pre=None, dx=None, ws=None):
     """Gradients of moe_block_norm for its inputs, from those of h (dh, as x) and n (dn, bf16); either
     may be None.  rstd: as moe_block_norm(stats=True) returned it; the other arguments as given there.
+    dx: where its gradient goes (as x), which may be dh, or None for a new tensor.
     Returns BlockNormGrads(dx, dy, dgate, dw_post, dw_pre), None for what was not given."""
     device, index = _on_gpu(x, "x")
     p, T, D = _norm_params(x, y, w_post, gate, gate_kind, gate_act, scale, w_pre, 1.0, index)
@@ -498,8 +499,10 @@ def moe_block_norm_backward(x, y, rstd, dh, dn, *, w_post=None, gate=None, gate_
     g = BlockNormGradParams()
     g.dh = _need(dh, "dh", x.dtype, (T, D), index)
     g.dn = _need(dn, "dn", torch.bfloat16, (T, D), index)
-    dx, dy, dgate, dw_post, dw_pre = torch.empty_like(x), None, None, None, None
-    g.dx = dx.data_ptr()
+    dy = dgate = dw_post = dw_pre = None
+    if dx is None:
+        dx = torch.empty_like(x)
+    g.dx = _need(dx, "dx", x.dtype, (T, D), index)
     if y is not None:
         dy = torch.empty_like(y)
         g.dy = dy.data_ptr()

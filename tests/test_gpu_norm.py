@@ -299,3 +299,21 @@ def test_no_tokens():
     assert r.n.shape == (0, 64)
     b = qm.moe_block_norm_backward(x, x, r.rstd, x, x, w_post=w, w_pre=w)
     assert (b.dw_post == 0).all() and (b.dw_pre == 0).all()
+
+
+@pytest.mark.parametrize("T,D,x_dt", [(7, 11, torch.bfloat16), (600, 515, torch.float32), (3, 5127, torch.bfloat16), (300, 8200, torch.float32)])
+def test_gradient_into_a_tensor_of_the_callers(T, D, x_dt):
+    d = gpu(make(T, D, x_dt, kind="element", act="sigmoid", seed=7))
+    kw = dict(w_post=d["w_post"], gate=d["gate"], gate_kind="element", gate_act="sigmoid", w_pre=d["w_pre"])
+    r = qm.moe_block_norm(d["x"], d["y"], stats=True, **kw)
+    b = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, d["dh"], d["dn"], **kw)
+    buf = torch.full((T + 2, D), 7.0, dtype=x_dt, device="cuda")
+    for dh in (d["dh"], buf[1:-1]):                            # another tensor, and dh itself
+        buf[1:-1].copy_(d["dh"])
+        o = qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, dh, d["dn"], dx=buf[1:-1], **kw)
+        assert o.dx.data_ptr() == buf[1:-1].data_ptr()
+        assert all(torch.equal(got, want) for got, want in zip(o, b))
+        assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+    for bad in (buf, buf[1:-1].t(), torch.empty(T, D, dtype=torch.float16, device="cuda"), torch.empty(T, D, dtype=x_dt)):
+        with pytest.raises(ValueError, match="dx"):
+            qm.moe_block_norm_backward(d["x"], d["y"], r.rstd, d["dh"], d["dn"], dx=bad, **kw)
