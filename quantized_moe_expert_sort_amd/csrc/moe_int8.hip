@@ -18,6 +18,8 @@
 #include "moe_operands.h"
 #include "moe_rows.h"
 
+#include <type_traits>
+
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is written by the load-to-LDS copies
 
 namespace moe {
@@ -136,18 +138,22 @@ __device__ __forceinline__ void store_one(const Gemm& p, int64_t t, int c, float
 // A workgroup takes one 16-channel block (with an activation the gate block and the up block of
 // the same outputs) and 16 tokens; its waves split K and add their sums through LDS.  The weights
 // are read once, from packed blocks of whole lines, straight into the operand registers, up to
-// seven blocks (and as many of the gate) in flight per wave before the first MFMA.  Bound by the
-// weights' bytes: 7168 x 3584 at 1 token 7.5 us, 3584 x 3584 5.5 us, so 3.6 us that do not depend
-// on the bytes and 6.7 TB/s beyond (four blocks in flight and 16 waves: 7.8 and 5.7 us).
+// eight blocks (and as many of the gate) in flight per wave before the first MFMA; what is left of a
+// wave's share after whole trips of eight is asked for as it is.  Bound by the weights' bytes: 7168 x K at
+// 1 token, cold, us at K 512, 1024, 2048, 3584, 4096, 5120, 7168, 8192: 3.8, 4.3, 5.1, 7.0, 7.5, 9.1, 11.5, 12.9;
+// six in flight 3.2, 4.2, 5.2, 7.2, 7.9, 8.4, 11.5, 12.2; the last trip filled up with repeated blocks 3.7, 4.3, 5.5,
+// 7.2, 7.8, 10.9, 12.6, 13.0, and with seven in flight 3.8, 4.4, 5.5, 7.1, 9.2, 10.7, 11.8, 14.4.
 
-constexpr int STREAM_U = 7;                   // K blocks a wave loads together
+constexpr int STREAM_U = 8;                   // K blocks a wave loads together
 constexpr int STREAM_WAVES = 8;               // waves of a workgroup, at most
 
 template <bool ACT>
 __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_i8_stream_kernel(const Gemm p, int blocks_k) {
   constexpr int NB = ACT ? 2 : 1;
   __shared__ v4i sums[STREAM_WAVES][NB][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  // the wave's number in a scalar register: what it decides are branches, and an MFMA under a lane mask
+  // would run with the mask ignored
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int r = lane & 15, g = lane >> 4;
   const uint8_t* wp[NB];
 #pragma unroll
@@ -160,24 +166,29 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_i8_stream_kernel(const
   const int steps = (p.K + 63) / 64;                          // the padding past them is not read
   const int per = (steps + waves - 1) / waves;
   const int s1 = min((wave + 1) * per, steps);
-  for (int s0 = wave * per; s0 < s1; s0 += STREAM_U) {
+  // blocks s0 .. s0 + STREAM_U - 1, or (not whole) as many of them as this wave has left
+  const auto trip = [&](const int s0, auto whole) {
     uint4 wv[STREAM_U][NB], av[STREAM_U];
 #pragma unroll
     for (int j = 0; j < STREAM_U; ++j) {
-      const int s = min(s0 + j, s1 - 1);
+      const int s = s0 + j;
+      if (!decltype(whole)::value && s >= s1) break;
 #pragma unroll
       for (int b = 0; b < NB; ++b) wv[j][b] = ldw16(wp[b] + (int64_t)s * 1024);
       av[j] = *reinterpret_cast<const uint4*>(ap + min(s * 64 + g * 16, p.K - 16));   // past K the weights are zero
     }
 #pragma unroll
-    for (int j = 0; j < STREAM_U; ++j)
-      if (s0 + j < s1) {
+    for (int j = 0; j < STREAM_U; ++j) {
+      if (!decltype(whole)::value && s0 + j >= s1) break;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wv[j][b]), __builtin_bit_cast(v4i, av[j]),
-                                                         acc[b], 0, 0, 0);
-      }
-  }
+      for (int b = 0; b < NB; ++b)
+        acc[b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, wv[j][b]), __builtin_bit_cast(v4i, av[j]),
+                                                       acc[b], 0, 0, 0);
+    }
+  };
+  int s0 = wave * per;
+  for (; s0 + STREAM_U <= s1; s0 += STREAM_U) trip(s0, std::true_type());
+  if (s0 < s1) trip(s0, std::false_type());
 #pragma unroll
   for (int b = 0; b < NB; ++b) sums[wave][b][lane] = acc[b];
   __syncthreads();
@@ -488,10 +499,17 @@ void tile(const Gemm& p, int blocks_k, hipStream_t s) {
 
 // Up to 16 tokens the weights are streamed; beyond, the smallest tiles that one round of CUS
 // workgroups holds (they take K in more groups), then the largest of which there is more than a
-// round.  Measured, K 3584, us: 64 tokens x 7168 (gate, up): streamed 15.6, 32 x 64 10.3, 64 x 64 in two
-// groups 12.2.  256 x 3584: 32 x 64 14.8, 64 x 64 in two groups 10.4, in one 12.1, 128 x 128 18.  256 x
-// 7168: 64 x 64 in two groups 22.8, in one 15.6, 128 x 128 18.2.  384 x 7168: 28.3, 19.3 (128 x 128).  512 x
-// 7168: 30, 21, 29 (256 x 256 in halves).  1024 x 7168: 56, 40, 34.
+// round.  Measured, us, chosen ones in brackets, in the order 32 x 64 in four groups, 64 x 64 in two, 64 x 64,
+// 128 x 128, 256 x 256 (with halves):
+//   K 512:   64 x 7168 [4.1] 4.6 4.4 5.9 8.1    256 x 3584 6.6 [4.7] 4.6 6.3 8.8    256 x 7168 11.6 7.8 [5.5] 6.5 9.0
+//           384 x 7168 16.6 10.9 8.1 [6.8] 9.2   1024 x 7168 37.4 23.5 15.4 12.5 [11.0]
+//   K 1456:  64 x 7168 [6.7] 8.2 7.7 10.6 15.4   256 x 3584 9.3 [6.7] 6.9 10.1 14.7   256 x 7168 19.8 13.7 [11.6] 12.4 17.8
+//           384 x 7168 25.2 18.6 15.3 [12.6] 17.8   1024 x 7168 69.1 44.2 31.0 25.2 [20.0]
+//   K 3584:  64 x 7168 [10.2] 12.6 12.1 17.6 27   256 x 3584 16.4 [11.5] 11.8 19.1 28.7   256 x 7168 31 21.7 [18.5] 20.4 29.7
+//           384 x 7168 38.6 29.6 26.1 [20.7] 30   1024 x 7168 104 68 57 41.5 [33.8]
+//   K 7168:  64 x 7168 [17.1] 21.5 20.9 30.6 47.6   256 x 3584 27.3 [19.5] 20.1 34.3 51.5   256 x 7168 51 36.7 [32.6] 35.3 52
+//           384 x 7168 64.8 50.4 46.4 [35.4] 51.9   1024 x 7168 176 117 100 72.3 [59.6]
+// Streamed at more tokens: 64 x 7168 (gate, up), K 3584: 15.6.
 template <bool ACT>
 void run(const Gemm& p, int blocks_k, hipStream_t s) {
   constexpr int CUS = 256;

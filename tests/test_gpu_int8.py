@@ -186,3 +186,10 @@ def test_situv2_of_small_values(T, small):
     want = 4.0 * torch.tanh(gate / 4.0) * torch.sigmoid(gate) * 25.0 * torch.tanh(up / 25.0)
     bad = (ref.f64(out) - want).abs() > (ref.HALF_BF16 + 2 * 2.0 ** -15 + 32 * ref.HALF_F32 * (1 + gate.abs())) * want.abs()
     assert not bad.any(), (int(bad.sum()), gate[bad][:4].tolist(), up[bad][:4].tolist())
+
+
+# a wave's share of K: less than one trip of eight blocks, just one, one and a part, several and a part
+@pytest.mark.parametrize("K", [448, 512, 528, 3584, 3600, 4080, 4096, 4112, 4608, 7168, 8192, 8208, 12304])
+def test_depths_of_few_tokens(K):
+    for T, act in ((1, None), (16, "silu"), (7, "situv2")):
+        check(T, 96, K, act, add=act is None)
