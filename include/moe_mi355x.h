@@ -392,8 +392,8 @@ typedef struct {
 } moe_block_norm_t;
 
 /* moe_block_norm -- the norm after one block, its gate, the residual sum and the norm before the
- * next block, with the normed rows coded for what reads them, in one launch and one pass over
- * the rows.  With rms(v) = sqrt(mean(v^2) + eps):
+ * next block, with the normed rows coded for what reads them, in one launch (several beyond 2^31
+ * work items, 64 to 1024 a row) and one pass over the rows.  With rms(v) = sqrt(mean(v^2) + eps):
  *     z = y / rms(y) * w_post  (z = y without w_post);   g = gate or sigmoid(gate), 1 without one
  *     h = x + scale * g * z    (h = x without y);        n = h / rms(h) * w_pre
  * computed in fp32 from the given rows; h, n and q are each rounded once, from fp32 (n and q come
@@ -429,8 +429,9 @@ static inline size_t moe_block_norm_backward_ws_bytes(int32_t tokens, int32_t di
  *   p         the forward call's struct: x, y, w_post, gate, w_pre, rstd (as the forward call wrote
  *             it) and the options; h, n, q and q_scale are not read.  rstd is needed when w_post or
  *             dn is given, w_pre when dn is.
- * One of dh and dn is given.  Sums over tokens are added in a fixed order.  tokens == 0 sets the
- * sums over tokens (dw_post, dw_pre, a per-channel dgate) to zero. */
+ * One of dh and dn is given.  Sums over tokens are added in a fixed order, at most 128 tokens in one
+ * register: beyond 32768 tokens (2^19 of narrow rows) they are taken in several launches.
+ * tokens == 0 sets the sums over tokens (dw_post, dw_pre, a per-channel dgate) to zero. */
 moe_status_t moe_block_norm_backward(const moe_block_norm_t *p, const moe_block_norm_grads_t *d, void *ws,
                                      size_t ws_bytes, void *stream);
 

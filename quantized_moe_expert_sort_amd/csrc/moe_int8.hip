@@ -224,9 +224,10 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_i8_stream_kernel(const
 // Measured (cold weights and tokens, K 3584): one round of tiles on 256 CUs takes 8.1 us at 32 x 64
 // (KG 4), 10.2 at 64 x 64 (KG 2), 11.6 at 64 x 64, 18 at 128 x 128, 28 at 128 x 256 and 48 at
 // 256 x 256: the smaller the tile, the more it is bound by the copies, which run at 45 to 50 bytes
-// a nanosecond and CU (140 from a warm L2).  At 8192^3 the 256 x 256 tiles reach 2410 TOP/s (the
-// matrix cores busy 61% of the time at 1.74 GHz, the clock the power limit leaves); without the
-// copies the same loop runs 1.5 times as fast, without the MFMAs 1.2 times.
+// a nanosecond and CU (140 from a warm L2).  At 8192^3 the 256 x 256 tiles take 489 us in the first launch
+// of a row (2250 TOP/s; a library product 2029) and 523 in the sixth: the clock falls from 1.8 to 1.54 GHz
+// and the share of the time that the matrix cores are busy rises from 56 to 63%.  8192 x 7168 x 3584 with
+// SiTUv2: 225 us, 1.9 GHz, 45%.  Without the copies the loop runs 1.5 times as fast, without the MFMAs 1.2 times.
 
 __device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");

@@ -15,13 +15,14 @@
 // over the rows a workgroup takes, written as partial sums and added in a fixed order by a second
 // launch, so that the gradients do not depend on timing.
 //
-// Measured on MI355X (a 2 GiB copy runs at 4.9 TB/s): forward 8192 x 3584 bf16 with fp8 codes 51 us
-// (265 MB: 54 us at the copy's rate), 4096 x 3584 with an fp32 stream 37 us (176 MB), one row 3.3 us;
-// backward 4096 x 3584, fp32 stream, gate per channel 48 us and 4.5 for the partial sums (264 MB).
-// Widths that 8 does not divide: 8192 x 3585 with a gate per element 46 us (36 at 3584), its backward
-// pass 86 (71); 4096 x 8191 57 (45) and 102 (77).
-// Rows of more than 8192 elements fill a lane's 128 registers in the backward pass (about 14 spilled
-// with a gate per channel or element): 1000 x 12000 bf16 41 and 45 us, 31 without a gate.
+// Measured on MI355X (medians of traced launches; a 2 GiB copy runs at 4.9 TB/s): forward 8192 x 3584 bf16,
+// gate per token, 57 us with fp8 codes (265 MB, 54 us at the copy's rate), 48 with fp4 and 50 with int8 codes;
+// 4096 x 3584 with an fp32 stream 38 us (176 MB), one row 3.2 us; backward 4096 x 3584, fp32 stream, gate per
+// channel 50 us and 4.7 for the partial sums (264 MB).  Widths that 8 does not divide: 8192 x 3585 with a
+// sigmoid gate per element 72 us (54 at 3584), its backward pass 134 (110); 4096 x 8191 backward 157.
+// Rows of more than 8192 elements fill a lane's 128 registers in the backward pass (17 to 21 spilled with a
+// gate per channel or element, 28 where 8 does not divide the width): 1000 x 12000 bf16 65 us with a sigmoid
+// gate per channel, 78 per element, 49 without a gate.
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
@@ -101,8 +102,8 @@ __device__ __forceinline__ float sigmoid_f(float x) {
 // Where D is no multiple of 8 (SHORT) one lane's last piece is short: it reads the VEC elements that end with
 // the row and moves its own down, zeros behind them (own_part, only in the wave that holds that
 // piece).  Lanes past the row read the same ones, for others to replace.
-// Kernels of their own for SHORT rows: with the branch on it the backward pass of 8192 x 3584 took 54
-// us, 51.5 without; 8192 x 3585 takes 63 us, and 153 in single elements.
+// Kernels of their own for SHORT rows: with the branch on it the backward pass of whole pieces took 54 us
+// instead of 51.5; single elements instead of the moved piece took 2.4 times as long at 8192 x 3585.
 template <int VEC, class T>
 __device__ __forceinline__ void load_at(const T* row, int col, int D, float (&v)[VEC]) {
   load_any<VEC>(el(row, min(col, D - VEC)), v);

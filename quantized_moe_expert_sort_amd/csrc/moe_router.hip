@@ -14,15 +14,18 @@
 // Choosing K of E: a bound that at least K keys reach is found among the 64 lane maxima (a search
 // over the bits of the key, one ballot a bit), the keys at or above it (K to K + a few of 896)
 // are compacted to one per lane through LDS, and every lane counts how many of them come before
-// its own.  Rows where more than 64 keys reach the bound (long runs of equal keys) take K rounds of
-// a maximum over the wave instead.  With a bias the keys are sums whose order could depend on
-// rounding, so the compacted candidates (taken with a margin for the fp32 error) are ranked by keys
-// in 64 bits.
+// its own.  Rows where more than 64 keys reach the bound (a large K, long runs of equal keys) take those
+// from the K-th largest key on instead, of experts equal to it the lowest.  With a bias the keys are sums
+// whose order could depend on rounding, so the compacted candidates (taken with a margin for the fp32
+// error) are ranked by keys in 64 bits; where more than 64 keys lie within that error of the K-th, K
+// maxima over the wave choose.
 //
-// Measured on MI355X: 16384 x 896 bf16, K 16: 14 us (29 MB, 6 us at a copy's 4.9 TB/s): bound by its
-// instructions and their latency (ordered integer keys and the rare paths in registers: 22 us);
-// 16 rows with a bias 6.2 us.  8192 x 896 fp32 with the balance statistics 16 us and 4.7 for the sums of
-// the workgroups' parts (29 MB); its backward pass 15 us (59 MB, 12 us), bound by the bytes.
+// Measured on MI355X (medians of traced launches): 16384 x 896 bf16, K 16: 15 us (29 MB, 6 us at a copy's
+// 4.9 TB/s): bound by its instructions and their latency (ordered integer keys and the rare paths in
+// registers: 22 us); 16 rows with a bias 6.3 us, 8192 x 896 fp32 with one 26.  8192 x 896 fp32 with the balance
+// statistics 17 us and 5.4 for the sums of the workgroups' parts (29 MB); its backward pass 16 us (59 MB, 12 us),
+// bound by the bytes.  Of all its kernels only those for more than 1024 experts that 8 does not divide, with a
+// bias and statistics, spill registers (61; 3040 x 1177 43 us, 24 without statistics).
 #include "moe_kernels.h"
 #include "moe_rows.h"
 
@@ -182,8 +185,8 @@ __device__ __forceinline__ float key_margin(float bound) { return 1e-5f * (1.0f 
 // half the lanes): those that reach the K-th largest key, of experts with the same logit and bias as it
 // only the K with the lowest numbers (the others cannot be chosen).  Returns how many; the first CAND
 // of them are in cand.  Without a bias they are fewer than 2 K <= CAND.
-// 3400 x 2048, K 32 (about one row in 50 comes here) 22 us, 172 with K maxima over the whole row
-// instead; 16384 x 896 of zeros (every row comes here) 32 us.
+// 3400 x 2048 fp32, K 32 (about one row in 50 comes here) 24 us, 172 with K maxima over the whole row
+// instead; 16384 x 896 of zeros (every row comes here) 33 us.
 template <class LT, int VEC, int NREG, bool BIAS>
 __device__ __forceinline__ int collect_from_kth(const LT* row, const float (&l)[NREG], const float (&keys)[BIAS ? NREG : 1],
                                                 const float* bias, int E, int K, int score, float m, float z,
@@ -419,7 +422,7 @@ __global__ __launch_bounds__((64 * router_waves<NREG, BIAS, BAL>())) void router
   const auto take = [&](const int64_t t) {
     const LT* const row = static_cast<const LT*>(a.logits) + t * a.E;
     // opaque where it is short of registers: the columns' addresses and masks would be kept over the rows
-    // and spill (3040 x 1177 with a bias 26 us, 41 with them kept)
+    // and spill (3040 x 1177 with a bias 24 us, 41 with them kept)
     int lane = lane0;
     if constexpr ((BIAS || BAL) && NREG > (VEC == 1 ? 4 : 16)) asm volatile("" : "+v"(lane));
     int id = -1;
