@@ -537,6 +537,123 @@ moe_status_t moe_gemm_i8(const int8_t *a, const float *a_scale, const int8_t *w_
                          int32_t tokens, int32_t out_features, int32_t in_features, const moe_act_params_t *act,
                          const uint16_t *add, uint16_t *out_bf16, void *stream);
 
+typedef struct {
+  const void *x;        /* [tokens, dim] residual stream, bf16 or fp32 (x_dt) */
+  const uint16_t *y;    /* [tokens, dim] bf16 output of a block, added to x, or NULL */
+  const float *w, *b;   /* [dim] weight and bias, or NULL (ones, zeros) */
+  void *h;              /* out [tokens, dim] as x: x + y, or NULL; may be x */
+  uint16_t *n;          /* out [tokens, dim] bf16 normed rows, or NULL */
+  void *q;              /* out: their codes (q_dt), or NULL */
+  void *q_scale;        /* out: their scales; NULL iff q is */
+  float *stats;         /* out [2, tokens]: mean and 1/deviation of h's rows, for the backward pass, or NULL */
+  int32_t tokens, dim;
+  int32_t x_dt;         /* MOE_DT_BF16 or MOE_DT_F32 */
+  int32_t q_dt;         /* MOE_DT_FP8_E4M3, MOE_DT_FP4_E2M1 or MOE_DT_I8; read only when q is given */
+  float eps;            /* a normal number > 0 */
+} moe_layer_norm_t;
+
+/* moe_layer_norm -- the residual sum and a layer norm of it, in one launch (several beyond 2^31 work
+ * items) and one pass over the rows:
+ *     h = x + y  (x without y);   n = (h - mean(h)) / sqrt(var(h) + eps) * w + b
+ * computed in fp32, the variance from the deviations; h, n and q are each rounded once, from fp32 (n and q
+ * come from h before its rounding).  Codes, shapes, alignment and Inf / NaN as in moe_block_norm. */
+moe_status_t moe_layer_norm(const moe_layer_norm_t *p, void *stream);
+
+typedef struct {
+  const void *dh;       /* [tokens, dim] as x: gradient of h, or NULL (zero); may be dx */
+  const uint16_t *dn;   /* [tokens, dim] bf16 gradient of n (of q's values too) */
+  void *dx;             /* out [tokens, dim] as x: gradient of x */
+  uint16_t *dy;         /* out [tokens, dim] bf16: the same, for y; given iff y is */
+  float *dw, *db;       /* out [dim], each or NULL */
+} moe_layer_norm_grads_t;
+
+/* Workspace of moe_layer_norm_backward: one row of partial sums per workgroup for each of dw and db. */
+static inline size_t moe_layer_norm_backward_ws_bytes(int32_t tokens, int32_t dim) {
+  size_t parts = tokens < MOE_NORM_PARTS ? (size_t)(tokens > 0 ? tokens : 0) : MOE_NORM_PARTS;
+  return moe_align256(parts * 2 * (size_t)dim * 4);
+}
+
+/* moe_layer_norm_backward -- gradients of moe_layer_norm for its inputs, given those of h and n.
+ *   p         the forward call's struct: x, y, w, stats (as the forward call wrote it) and the sizes;
+ *             b, h, n, q and q_scale are not read.
+ * Sums over tokens are added in a fixed order, as in moe_block_norm_backward.  tokens == 0 sets dw and db
+ * to zero. */
+moe_status_t moe_layer_norm_backward(const moe_layer_norm_t *p, const moe_layer_norm_grads_t *d, void *ws,
+                                     size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Microscaled matrices: fp8 e4m3 or fp4 e2m1 codes with one e8m0 scale per 32 along a row, and the
+ * product of such tokens with MXFP4 weights.  Rows of codes are filled up with zeros to a multiple of
+ * 128 columns, so matrices of any size can be coded and multiplied.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Columns of a coded row. */
+static inline int64_t moe_mx_padded_k(int64_t cols) { return (cols + 127) / 128 * 128; }
+
+/* ROWS: codes [rows, padded_k] bytes (fp8) or [rows, padded_k / 2] (fp4x2), scales [rows, padded_k / 32];
+ * the layout of moe_quant_act where cols % 128 == 0.  PACKED (fp4 weights of moe_gemm_mx): blocks (f, s) of rows
+ * 16 f .. 16 f + 15 and columns 128 s .. 128 s + 127, s fastest: 1 KB of codes, byte 16 (16 g + r) + b being
+ * columns 128 s + 32 g + 2 b and + 1 of row 16 f + r, as moe_pack_w1 writes them, and 64 bytes of scales, byte
+ * 4 r + g; zero past the matrix. */
+typedef enum { MOE_MX_ROWS = 0, MOE_MX_PACKED = 1 } moe_mx_layout_t;
+
+static inline size_t moe_mx_packed_bytes(int32_t rows, int32_t cols) {
+  return (size_t)(((int64_t)rows + 15) / 16 * 16) * (size_t)(moe_mx_padded_k(cols) / 2);
+}
+static inline size_t moe_mx_packed_scale_bytes(int32_t rows, int32_t cols) {
+  return (size_t)(((int64_t)rows + 15) / 16 * 16) * (size_t)(moe_mx_padded_k(cols) / 32);
+}
+
+typedef struct {
+  const void *x;        /* [rows, cols], bf16 or fp32 (x_dt) */
+  const uint8_t *noise; /* [rows, cols] uniform random bytes: stochastic rounding; or NULL: to nearest */
+  void *q;              /* out: codes of x's rows, or NULL */
+  uint8_t *q_scale;     /* out: their scales; NULL iff q is */
+  void *t;              /* out: codes of the rows of x's transpose [cols, rows], or NULL */
+  uint8_t *t_scale;     /* out: their scales; NULL iff t is */
+  int32_t rows, cols;
+  int32_t x_dt;         /* MOE_DT_BF16 or MOE_DT_F32 */
+  int32_t q_dt, q_layout;   /* MOE_DT_FP8_E4M3 or MOE_DT_FP4_E2M1, moe_mx_layout_t; read only when q is given */
+  int32_t t_dt, t_layout;   /* the same of t */
+} moe_quant_mx_t;
+
+/* moe_quant_mx -- microscaled codes of a matrix along its rows, along its columns, or both in one pass
+ * over it, by the rule of moe_quant_act from the given values (fp32 too).  With noise n an element goes to
+ * one of the two neighbours on the grid: its magnitude in units of its last place is
+ * floor(|x| / 2^s + (2 n + 1) / 512) (saturated values stay), the same n for both codings.
+ * What a linear layer Y = X W^T trained with such products takes: X and W coded along their rows for Y;
+ * dY along its rows and W along its columns for dX = dY W; dY and X along their columns for
+ * dW = dY^T X.
+ * q and t 16-byte aligned (else MOE_ERR_INVALID_ARG); PACKED needs fp4 (else MOE_ERR_UNSUPPORTED).
+ * rows and cols below 2^31 - 256, their product below 2^40; rows == 0 returns MOE_OK. */
+moe_status_t moe_quant_mx(const moe_quant_mx_t *p, void *stream);
+
+/* moe_pack_mx -- MXFP4 weights as a checkpoint stores them, codes [out_features, in_features / 2] and scales
+ * [out_features, in_features / 32], reordered once into the PACKED layout.  in_features % 32 == 0, packed
+ * bytes < 2^32 (else MOE_ERR_UNSUPPORTED); w and w_packed 16-byte aligned, the outputs apart from the inputs (else
+ * MOE_ERR_INVALID_ARG). */
+moe_status_t moe_pack_mx(const uint8_t *w, const uint8_t *w_scale, int32_t out_features, int32_t in_features,
+                         uint8_t *w_packed, uint8_t *w_scale_packed, void *stream);
+
+/* moe_gemm_mx -- product of coded tokens and packed MXFP4 weights, in fp32:
+ *     r[t, c] = sum_k a[t, k] w[c, k]   (the values that codes and scales stand for)
+ *     out = r (+ add), or with act: out[t, i] = act(r[t, i], r[t, O/2 + i]) (+ add), O = out_features
+ *             (gate rows first, then the up rows).
+ *   a         [tokens, in_features] fp8 or fp4x2 codes (a_dtype), a_scale [tokens, in_features / 32]; as
+ *             moe_quant_mx (ROWS), moe_quant_act, moe_block_norm or moe_layer_norm write them.
+ *             in_features is the padded width, a multiple of 128 (else MOE_ERR_UNSUPPORTED).
+ *   w         PACKED, of out_features rows and in_features columns; w_scale its scales.
+ *   act       or NULL; MOE_ACT_SITUV2 or MOE_ACT_SILU, then out_features % 32 == 0.
+ *   add       shape and type of out, or NULL; may be out.
+ *   out       [tokens, out_features], or [tokens, out_features / 2] with act, bf16 or fp32 (out_dtype); bf16 is
+ *             rounded once from fp32.
+ * A scale byte of 255 (a block that held Inf or NaN) makes its row's or its channel's results NaN.
+ * a and w 16-byte, the scales 4-byte aligned (else MOE_ERR_INVALID_ARG).  in_features < 2^24, tokens < 2^24, packed
+ * bytes < 2^32, tokens * max(in_features, out_features) < 2^40 (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_gemm_mx(const void *a, const uint8_t *a_scale, int32_t a_dtype, const uint8_t *w, const uint8_t *w_scale,
+                         int32_t tokens, int32_t out_features, int32_t in_features, const moe_act_params_t *act,
+                         const void *add, void *out, int32_t out_dtype, void *stream);
+
 /* The hipError_t value behind the last MOE_ERR_HIP returned on this thread (0 if none). */
 int32_t moe_last_hip_error(void);
 

@@ -30,7 +30,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi35
 DEBUG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_mi355x_debug.so")
 EXPORTS = ("moe_sort", "moe_quant_act", "moe_pack_w1", "moe_pack_w2", "moe_fused", "moe_fused_noalloc",
            "moe_block_norm", "moe_block_norm_backward", "moe_router", "moe_router_backward", "moe_quant_i8",
-           "moe_pack_i8", "moe_gemm_i8", "moe_last_hip_error")
+           "moe_pack_i8", "moe_gemm_i8", "moe_layer_norm", "moe_layer_norm_backward", "moe_quant_mx", "moe_pack_mx",
+           "moe_gemm_mx", "moe_last_hip_error")
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 
@@ -75,6 +76,20 @@ class BalanceParams(ctypes.Structure):
                 + [(n, ctypes.c_void_p) for n in ("counts", "mean_prob", "loss", "num_valid")])
 
 
+class LayerNormParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "y", "w", "b", "h", "n", "q", "q_scale", "stats")]
+                + [(n, ctypes.c_int32) for n in ("tokens", "dim", "x_dt", "q_dt")] + [("eps", ctypes.c_float)])
+
+
+class LayerNormGradParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dh", "dn", "dx", "dy", "dw", "db")]
+
+
+class QuantMxParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "noise", "q", "q_scale", "t", "t_scale")]
+                + [(n, ctypes.c_int32) for n in ("rows", "cols", "x_dt", "q_dt", "q_layout", "t_dt", "t_layout")])
+
+
 _lib = None
 
 
@@ -115,6 +130,16 @@ def lib():
         L.moe_pack_i8.restype = i32
         L.moe_gemm_i8.argtypes = [vp, vp, vp, vp, i32, i32, i32, ctypes.POINTER(ActParams), vp, vp, vp]
         L.moe_gemm_i8.restype = i32
+        L.moe_layer_norm.argtypes = [ctypes.POINTER(LayerNormParams), vp]
+        L.moe_layer_norm.restype = i32
+        L.moe_layer_norm_backward.argtypes = [ctypes.POINTER(LayerNormParams), ctypes.POINTER(LayerNormGradParams), vp, sz, vp]
+        L.moe_layer_norm_backward.restype = i32
+        L.moe_quant_mx.argtypes = [ctypes.POINTER(QuantMxParams), vp]
+        L.moe_quant_mx.restype = i32
+        L.moe_pack_mx.argtypes = [vp, vp, i32, i32, vp, vp, vp]
+        L.moe_pack_mx.restype = i32
+        L.moe_gemm_mx.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, ctypes.POINTER(ActParams), vp, vp, i32, vp]
+        L.moe_gemm_mx.restype = i32
         L.moe_last_hip_error.argtypes = []
         L.moe_last_hip_error.restype = i32
         _lib = L
@@ -644,4 +669,194 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
           _need(w_packed, "w_packed", torch.int8, i8_packed_shape(N, K), index),
           _need(w_scale, "w_scale", torch.float32, (N,), index), T, N, K, params,
           _need(add, "add", torch.bfloat16, shape, index), _need(out, "out", torch.bfloat16, shape, index))
+    return out
+
+
+# ------------------------------------------------------------------ layer norm
+
+LayerNorm = collections.namedtuple("LayerNorm", "h n q q_scale stats")
+LayerNormGrads = collections.namedtuple("LayerNormGrads", "dx dy dw db")
+
+
+def layer_norm_backward_ws_bytes(tokens, dim):
+    return _align256(min(max(tokens, 0), NORM_PARTS) * 2 * dim * 4)
+
+
+def _layer_norm_params(x, y, w, eps, index):
+    if x.dim() != 2 or x.dtype not in _ROW_TYPES:
+        raise ValueError(f"x: need a bfloat16 or float32 tensor [tokens, dim], got {x.dtype} of {tuple(x.shape)}")
+    T, D = x.shape
+    _sizes(T, D)
+    p = LayerNormParams(tokens=T, dim=D, x_dt=_ROW_TYPES[x.dtype], eps=eps)
+    p.x = _need(x, "x", x.dtype, (T, D), index)
+    p.y = _need(y, "y", torch.bfloat16, (T, D), index)
+    p.w = _need(w, "w", torch.float32, (D,), index)
+    return p, T, D
+
+
+def moe_layer_norm(x, y=None, *, w=None, b=None, eps=1e-5, h=None, want_n=True, q_dtype=None, stats=False):
+    """The residual sum x + y and a layer norm of it (see moe_layer_norm in the header).  x bf16 or fp32
+    [T, D], y bf16 [T, D], w and b fp32 [D].
+
+    Returns LayerNorm(h, n, q, q_scale, stats): h as x (None without y; pass h=x to update the stream in
+    place), n bf16 (None with want_n=False), q and q_scale for q_dtype "fp8", "fp4" or "i8", stats [2, T]
+    with stats=True (the backward pass needs them)."""
+    device, index = _on_gpu(x, "x")
+    p, T, D = _layer_norm_params(x, y, w, eps, index)
+    p.b = _need(b, "b", torch.float32, (D,), index)
+    n = q = q_scale = st = None
+    if h is not None:
+        p.h = _need(h, "h", x.dtype, (T, D), index)
+    elif y is not None:
+        h = torch.empty_like(x)
+        p.h = h.data_ptr()
+    if want_n:
+        n = torch.empty(T, D, dtype=torch.bfloat16, device=device)
+        p.n = n.data_ptr()
+    if q_dtype is not None:
+        p.q_dt = _pick(Q_DTYPES, q_dtype, "q_dtype")
+        if p.q_dt == DT_I8:
+            q = torch.empty(T, D, dtype=torch.int8, device=device)
+            q_scale = torch.empty(T, dtype=torch.float32, device=device)
+        else:
+            q = torch.empty(T, D if p.q_dt == DT_FP8 else D // 2, dtype=torch.uint8, device=device)
+            q_scale = torch.empty(T, D // 32, dtype=torch.uint8, device=device)
+        p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
+    if stats:
+        st = torch.empty(2, T, dtype=torch.float32, device=device)
+        p.stats = st.data_ptr()
+    _call("moe_layer_norm", index, p)
+    return LayerNorm(h, n, q, q_scale, st)
+
+
+def moe_layer_norm_backward(x, y, stats, dh, dn, *, w=None, bias=True, dx=None, ws=None):
+    """Gradients of moe_layer_norm for its inputs, from those of h (dh, as x, or None) and n (dn, bf16).
+    stats: as moe_layer_norm(stats=True) returned them; x, y and w as given there; bias: whether db is
+    wanted.  dx: where its gradient goes (as x), which may be dh, or None for a new tensor.
+    Returns LayerNormGrads(dx, dy, dw, db), None for what was not given or wanted."""
+    device, index = _on_gpu(x, "x")
+    p, T, D = _layer_norm_params(x, y, w, 1.0, index)
+    p.stats = _need(stats, "stats", torch.float32, (2, T), index)
+    if dn is None:
+        raise ValueError("dn: the gradient of n is needed")
+    g = LayerNormGradParams()
+    g.dh = _need(dh, "dh", x.dtype, (T, D), index)
+    g.dn = _need(dn, "dn", torch.bfloat16, (T, D), index)
+    dy = dw = db = None
+    if dx is None:
+        dx = torch.empty_like(x)
+    g.dx = _need(dx, "dx", x.dtype, (T, D), index)
+    if y is not None:
+        dy = torch.empty_like(y)
+        g.dy = dy.data_ptr()
+    if w is not None:
+        dw = torch.empty_like(w)
+        g.dw = dw.data_ptr()
+    if bias:
+        db = torch.empty(D, dtype=torch.float32, device=device)
+        g.db = db.data_ptr()
+    if ws is None:
+        ws = torch.empty(layer_norm_backward_ws_bytes(T, D), dtype=torch.uint8, device=device)
+    _call("moe_layer_norm_backward", index, p, g, _need(ws, "ws", torch.uint8, ws.shape, index), ws.numel())
+    return LayerNormGrads(dx, dy, dw, db)
+
+
+# ------------------------------------------------------------------ microscaled matrices
+
+MX_DTYPES = {"fp8": DT_FP8, "fp4": DT_FP4}
+MX_ROWS, MX_PACKED = 0, 1
+MxCodes = collections.namedtuple("MxCodes", "q q_scale t t_scale")
+
+
+def mx_padded_k(cols):
+    """Columns of a coded row: rows are filled up with zeros to one K step of the product."""
+    return (cols + 127) // 128 * 128
+
+
+def mx_shapes(rows, cols, dt, packed=False):
+    """Shapes of the codes (uint8) and scales of a matrix [rows, cols] coded along its rows."""
+    k = mx_padded_k(cols)
+    if packed:
+        return ((rows + 15) // 16, k // 128, 1024), ((rows + 15) // 16, k // 128, 64)
+    return (rows, k if dt == DT_FP8 else k // 2), (rows, k // 32)
+
+
+def moe_quant_mx(x, q_dtype=None, *, packed=False, t_dtype=None, t_packed=False, noise=None):
+    """Microscaled codes of a bf16 or fp32 matrix [R, C] along its rows (q_dtype "fp8" or "fp4"), of its
+    transpose's rows (t_dtype), or both in one pass (see moe_quant_mx in the header).  packed, t_packed: as
+    the weights of moe_gemm_mx ("fp4" only).  noise: uint8 [R, C] uniform random bytes for stochastic
+    rounding, or None for the nearest.
+
+    Returns MxCodes(q, q_scale, t, t_scale), None for what was not asked for."""
+    device, index = _on_gpu(x, "x")
+    if x.dim() != 2 or x.dtype not in _ROW_TYPES:
+        raise ValueError(f"x: need a bfloat16 or float32 tensor [rows, cols], got {x.dtype} of {tuple(x.shape)}")
+    R, C = x.shape
+    _sizes(R, C)
+    p = QuantMxParams(rows=R, cols=C, x_dt=_ROW_TYPES[x.dtype])
+    p.x = _need(x, "x", x.dtype, (R, C), index)
+    p.noise = _need(noise, "noise", torch.uint8, (R, C), index)
+    q = q_scale = t = t_scale = None
+    if q_dtype is not None:
+        p.q_dt, p.q_layout = _pick(MX_DTYPES, q_dtype, "q_dtype"), int(bool(packed))
+        shape, s_shape = mx_shapes(R, C, p.q_dt, packed)
+        q, q_scale = (torch.empty(s, dtype=torch.uint8, device=device) for s in (shape, s_shape))
+        p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
+    if t_dtype is not None:
+        p.t_dt, p.t_layout = _pick(MX_DTYPES, t_dtype, "t_dtype"), int(bool(t_packed))
+        shape, s_shape = mx_shapes(C, R, p.t_dt, t_packed)
+        t, t_scale = (torch.empty(s, dtype=torch.uint8, device=device) for s in (shape, s_shape))
+        p.t, p.t_scale = t.data_ptr(), t_scale.data_ptr()
+    if q_dtype is None and t_dtype is None:
+        raise ValueError("one of q_dtype and t_dtype is needed")
+    _call("moe_quant_mx", index, p)
+    return MxCodes(q, q_scale, t, t_scale)
+
+
+def moe_pack_mx(w, w_scale):
+    """MXFP4 weights, codes uint8 [N, K / 2] and e8m0 scales uint8 [N, K / 32], -> (codes, scales) in the
+    layout moe_gemm_mx reads."""
+    device, index = _on_gpu(w, "w")
+    if w.dim() != 2:
+        raise ValueError(f"w: need codes [out_features, in_features / 2], got {tuple(w.shape)}")
+    N, K = w.shape[0], 2 * w.shape[1]
+    _sizes(N, K)
+    shape, s_shape = mx_shapes(N, K, DT_FP4, True)
+    q, s = (torch.empty(v, dtype=torch.uint8, device=device) for v in (shape, s_shape))
+    _call("moe_pack_mx", index, _need(w, "w", torch.uint8, (N, K // 2), index),
+          _need(w_scale, "w_scale", torch.uint8, (N, K // 32), index), N, K, q.data_ptr(), s.data_ptr())
+    return q, s
+
+
+def moe_gemm_mx(a, a_scale, a_dtype, w, w_scale, out_features, *, act=None, beta=None, linear_beta=None, add=None, out=None,
+                out_dtype=torch.bfloat16):
+    """Tokens in "fp8" or "fp4" codes [T, ...] (scales [T, K / 32], K a multiple of 128) times packed MXFP4
+    weights of out_features rows (of moe_pack_mx, or moe_quant_mx with packed), with act "situv2" or "silu" of
+    the [gate|up] halves and `add` (shape and type of the result) in the same launch (see moe_gemm_mx in the
+    header).  Returns out, bf16 or fp32 (out_dtype; that of `out` where it is given)."""
+    device, index = _on_gpu(a, "a")
+    if a.dim() != 2:
+        raise ValueError(f"a: need codes [tokens, ...], got {tuple(a.shape)}")
+    dt = _pick(MX_DTYPES, a_dtype, "a_dtype")
+    T, K = a.shape[0], a.shape[1] * (2 if dt == DT_FP4 else 1)
+    N = out_features
+    _sizes(T, N, K)
+    params = None
+    if act is not None:
+        k = _pick(ACTS, act, "act")
+        if k == ACT_SITUV2 and (beta is None or linear_beta is None):
+            raise ValueError("SiTUv2 needs beta and linear_beta (there are no defaults)")
+        params = ActParams(k, 0.0 if beta is None else beta, 0.0 if linear_beta is None else linear_beta)
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _ROW_TYPES:
+        raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
+    shape = (T, N if act is None else N // 2)
+    if out is None:
+        out = torch.empty(*shape, dtype=out_dtype, device=device)
+    ws, wss = mx_shapes(N, K, DT_FP4, True)
+    _call("moe_gemm_mx", index, _need(a, "a", torch.uint8, a.shape, index),
+          _need(a_scale, "a_scale", torch.uint8, (T, K // 32), index), dt, _need(w, "w", torch.uint8, ws, index),
+          _need(w_scale, "w_scale", torch.uint8, wss, index), T, N, K, params,
+          _need(add, "add", out_dtype, shape, index), _need(out, "out", out_dtype, shape, index), _ROW_TYPES[out_dtype])
     return out

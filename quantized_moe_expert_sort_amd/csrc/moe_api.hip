@@ -445,4 +445,116 @@ moe_status_t moe_gemm_i8(const int8_t* a, const float* a_scale, const int8_t* w_
   return finish(hip_status(moe::launch_gemm_i8(g, (hipStream_t)stream)));
 }
 
+// What the forward and the backward pass of the layer norm both require; *a is filled.
+static moe_status_t check_layer_norm(const moe_layer_norm_t* p, moe::LayerNormArgs* a) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->dim <= 0 || !row_type(p->x_dt)) return MOE_ERR_INVALID_ARG;
+  if (!std::isnormal(p->eps) || p->eps <= 0.f) return MOE_ERR_INVALID_ARG;
+  if (p->dim > MOE_NORM_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+  if (p->tokens > 0 && !p->x) return MOE_ERR_INVALID_ARG;
+  *a = moe::LayerNormArgs{p->x, p->y, p->w, p->b, p->h, p->n, p->q, p->q_scale, p->stats,
+                          p->stats ? p->stats + p->tokens : nullptr, p->tokens, p->dim, p->x_dt, p->q_dt, p->eps};
+  return MOE_OK;
+}
+
+moe_status_t moe_layer_norm(const moe_layer_norm_t* p, void* stream) {
+  moe::LayerNormArgs a;
+  const moe_status_t st = check_layer_norm(p, &a);
+  if (st != MOE_OK) return st;
+  if ((p->q == nullptr) != (p->q_scale == nullptr) && p->tokens > 0) return MOE_ERR_INVALID_ARG;
+  if (p->q) {
+    if (p->q_dt != MOE_DT_FP8_E4M3 && p->q_dt != MOE_DT_FP4_E2M1 && p->q_dt != MOE_DT_I8) return MOE_ERR_INVALID_ARG;
+    if (p->dim % (p->q_dt == MOE_DT_I8 ? 16 : 32) != 0) return MOE_ERR_UNSUPPORTED;
+  }
+  if (p->tokens == 0) return MOE_OK;
+  if (!p->h && !p->n && !p->q && !p->stats) return MOE_ERR_INVALID_ARG;
+  if (p->q && !(aligned16(p->x) && aligned16(p->y) && aligned16(p->w) && aligned16(p->b) && aligned16(p->h) &&
+                aligned16(p->n) && aligned16(p->q)))
+    return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_layer_norm(a, (hipStream_t)stream)));
+}
+
+moe_status_t moe_layer_norm_backward(const moe_layer_norm_t* p, const moe_layer_norm_grads_t* d, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  moe::LayerNormBackwardArgs b;
+  const moe_status_t st = check_layer_norm(p, &b.f);
+  if (st != MOE_OK) return st;
+  if (!d) return MOE_ERR_INVALID_ARG;
+  if (p->tokens > 0) {
+    if (!d->dn || !d->dx || !p->stats || (d->dy == nullptr) != (p->y == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned4(ws)) return MOE_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < moe_layer_norm_backward_ws_bytes(p->tokens, p->dim)) return MOE_ERR_WORKSPACE;
+  b.dh = d->dh;
+  b.dn = d->dn;
+  b.dx = d->dx;
+  b.dy = d->dy;
+  b.dw = d->dw;
+  b.db = d->db;
+  b.part = (float*)ws;
+  return finish(hip_status(moe::launch_layer_norm_backward(b, (hipStream_t)stream)));
+}
+
+static bool code_type(int32_t dt) { return dt == MOE_DT_FP8_E4M3 || dt == MOE_DT_FP4_E2M1; }
+
+moe_status_t moe_quant_mx(const moe_quant_mx_t* p, void* stream) {
+  if (!p || p->rows < 0 || p->cols < 1 || !row_type(p->x_dt)) return MOE_ERR_INVALID_ARG;
+  if ((p->q == nullptr) != (p->q_scale == nullptr) || (p->t == nullptr) != (p->t_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+  const void* const out[2] = {p->q, p->t};
+  const int32_t dt[2] = {p->q_dt, p->t_dt}, layout[2] = {p->q_layout, p->t_layout};
+  for (int i = 0; i < 2; ++i) {
+    if (!out[i]) continue;
+    if (!code_type(dt[i]) || (layout[i] != MOE_MX_ROWS && layout[i] != MOE_MX_PACKED) || !aligned16(out[i]))
+      return MOE_ERR_INVALID_ARG;
+    if (layout[i] == MOE_MX_PACKED && dt[i] != MOE_DT_FP4_E2M1) return MOE_ERR_UNSUPPORTED;
+  }
+  const int64_t most = ((int64_t)1 << 31) - 256;
+  if (p->rows >= most || p->cols >= most || (int64_t)p->rows * p->cols >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (p->rows == 0) return MOE_OK;
+  if (!p->x || (!p->q && !p->t)) return MOE_ERR_INVALID_ARG;
+  const moe::QuantMxArgs a{p->x, p->noise, p->q, p->q_scale, p->t, p->t_scale, p->rows, p->cols, p->x_dt, p->q_dt,
+                           p->q_layout, p->t_dt, p->t_layout};
+  return finish(hip_status(moe::launch_quant_mx(a, (hipStream_t)stream)));
+}
+
+static bool apart(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return (uintptr_t)a + a_bytes <= (uintptr_t)b || (uintptr_t)b + b_bytes <= (uintptr_t)a;
+}
+
+moe_status_t moe_pack_mx(const uint8_t* w, const uint8_t* w_scale, int32_t out_features, int32_t in_features,
+                         uint8_t* w_packed, uint8_t* w_scale_packed, void* stream) {
+  if (!w || !w_scale || !w_packed || !w_scale_packed || out_features < 1 || in_features < 1 || !aligned16(w) || !aligned16(w_packed))
+    return MOE_ERR_INVALID_ARG;
+  const size_t packed = moe_mx_packed_bytes(out_features, in_features), scales = moe_mx_packed_scale_bytes(out_features, in_features);
+  if (in_features % 32 != 0 || packed >= ((size_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  const size_t wb = (size_t)out_features * (size_t)(in_features / 2), sb = (size_t)out_features * (size_t)(in_features / 32);
+  if (!apart(w, wb, w_packed, packed) || !apart(w, wb, w_scale_packed, scales) || !apart(w_scale, sb, w_packed, packed) ||
+      !apart(w_scale, sb, w_scale_packed, scales) || !apart(w_packed, packed, w_scale_packed, scales))
+    return MOE_ERR_INVALID_ARG;
+  return finish(hip_status(moe::launch_pack_mx(w, w_scale, out_features, in_features, w_packed, w_scale_packed, (hipStream_t)stream)));
+}
+
+moe_status_t moe_gemm_mx(const void* a, const uint8_t* a_scale, int32_t a_dtype, const uint8_t* w, const uint8_t* w_scale,
+                         int32_t tokens, int32_t out_features, int32_t in_features, const moe_act_params_t* act,
+                         const void* add, void* out, int32_t out_dtype, void* stream) {
+  if (tokens < 0 || out_features < 1 || in_features < 1 || !code_type(a_dtype) || !row_type(out_dtype)) return MOE_ERR_INVALID_ARG;
+  if (act) {
+    if (act->act != MOE_ACT_SITUV2 && act->act != MOE_ACT_SILU) return MOE_ERR_UNSUPPORTED;
+    if (act->act == MOE_ACT_SITUV2 &&
+        !(std::isfinite(act->beta) && act->beta > 0.f && std::isfinite(act->linear_beta) && act->linear_beta > 0.f))
+      return MOE_ERR_INVALID_ARG;
+    if (out_features % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  }
+  if (in_features % 128 != 0 || in_features >= (1 << 24) || tokens >= (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  if (moe_mx_packed_bytes(out_features, in_features) >= ((size_t)1 << 32)) return MOE_ERR_UNSUPPORTED;
+  const int32_t wider = in_features > out_features ? in_features : out_features;
+  if ((int64_t)tokens * wider >= ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
+  if (tokens == 0) return MOE_OK;
+  if (!a || !a_scale || !w || !w_scale || !out || !aligned16(a) || !aligned16(w) || !aligned4(a_scale) || !aligned4(w_scale))
+    return MOE_ERR_INVALID_ARG;
+  const moe::GemmMxArgs g{(const uint8_t*)a, a_scale, w, w_scale, add, out, tokens, out_features, in_features, a_dtype,
+                          act ? act->act : -1, out_dtype, act ? act->beta : 0.f, act ? act->linear_beta : 0.f};
+  return finish(hip_status(moe::launch_gemm_mx(g, (hipStream_t)stream)));
+}
+
 }  // extern "C"

@@ -16,6 +16,7 @@
 // token's row past K is multiplied by zero.
 #include "moe_kernels.h"
 #include "moe_operands.h"
+#include "moe_products.h"
 #include "moe_rows.h"
 
 #include <type_traits>
@@ -94,38 +95,15 @@ __global__ __launch_bounds__(256) void pack_i8_kernel(const uint8_t* __restrict_
 
 // ---------------------------------------------------------------- epilogue
 
-struct Gemm {
+struct Gemm : ActArgs {
   const uint8_t* a;        // [T, K]
   const float* sa;         // [T]
   const uint8_t* w;        // packed
   const float* sw;         // [N]
   const uint16_t* add;     // [T, No] or null
   uint16_t* out;           // [T, No]
-  int T, N, K, No, act;    // No = N, or N / 2 with an activation
-  float beta, inv_beta, lb, inv_lb;
+  int T, N, K, No;         // No = N, or N / 2 with an activation
 };
-
-// 1 - 2^s for s <= 0.  Near 0 the difference would keep only what 2^s holds beside 1 (1% at s = -1e-5); there
-// the first two terms of its series, off by s^2 / 12.5 < 2^-17 of it, beyond them 2^-24 of at least 2^-7.5.
-__device__ __forceinline__ float one_minus_exp2(float s) {
-  constexpr float LN2 = 0.6931471805599453f;
-  const float near = s * __builtin_fmaf(s, -0.5f * LN2 * LN2, -LN2);
-  return s > -0x1p-7f ? near : 1.0f - __builtin_amdgcn_exp2f(s);
-}
-// As situv2, with each tanh to a bf16's last place however small its argument.
-__device__ __forceinline__ float situv2_small(float g, float u, const Gemm& p) {
-  constexpr float LOG2E = 1.4426950408889634f;
-  const float ag = __builtin_fabsf(g), au = __builtin_fabsf(u);
-  const float a = one_minus_exp2(ag * (-2.0f * LOG2E * p.inv_beta));
-  const float b = __builtin_amdgcn_exp2f(ag * -LOG2E);
-  const float c = one_minus_exp2(au * (-2.0f * LOG2E * p.inv_lb));
-  const float d = 2.0f - a, den = __builtin_fmaf(d, b, d) * (2.0f - c);
-  const float y = (p.beta * p.lb) * (a * c * (g < 0.0f ? b : 1.0f)) * __builtin_amdgcn_rcpf(den);
-  return __builtin_copysignf(y, __uint_as_float(__float_as_uint(g) ^ __float_as_uint(u)));
-}
-__device__ __forceinline__ float activate(const Gemm& p, float g, float u) {
-  return p.act == MOE_ACT_SITUV2 ? situv2_small(g, u, p) : silu_mul(g, u);
-}
 
 // One output, channel c of token t.
 __device__ __forceinline__ void store_one(const Gemm& p, int64_t t, int c, float v) {
@@ -228,10 +206,6 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_i8_stream_kernel(const
 // of a row (2250 TOP/s; a library product 2029) and 523 in the sixth: the clock falls from 1.8 to 1.54 GHz
 // and the share of the time that the matrix cores are busy rises from 56 to 63%.  8192 x 7168 x 3584 with
 // SiTUv2: 225 us, 1.9 GHz, 45%.  Without the copies the loop runs 1.5 times as fast, without the MFMAs 1.2 times.
-
-__device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
-}
 
 template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
 struct Tile {
@@ -441,22 +415,6 @@ __device__ __forceinline__ void tile_body(const Gemm& p, int blocks_k, int tm, i
   }
 }
 
-// Tile number `id` of tiles_m x tiles_n: in columns of four tiles down the tokens, so that
-// neighbouring numbers share rows.
-__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int ROWS = 4;
-  const int per_group = ROWS * tiles_n, grp = id / per_group, in = id - grp * per_group;
-  const int rows = min(ROWS, tiles_m - grp * ROWS);
-  tm = grp * ROWS + in % rows;
-  tn = in / rows;
-}
-// Workgroup b runs on XCD b % 8: gives each XCD a run of consecutive numbers out of n, so that the
-// tiles it works on at one time share rows in its L2.
-__device__ __forceinline__ int run_of_xcd(int b, int n) {
-  const int x = b & 7, q = n >> 3, rem = n & 7;
-  return x * q + min(x, rem) + (b >> 3);
-}
-
 template <int BM, int BN, int GM, int GN, int S, int KG, bool ACT>
 __global__ __launch_bounds__(GM * GN * KG * 64) void gemm_i8_tile_kernel(const Gemm p, int blocks_k, int tiles_m, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Tile<BM, BN, GM, GN, S, KG, ACT>::LDS];
@@ -563,12 +521,8 @@ hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t s) {
   p.T = a.T;
   p.N = a.N;
   p.K = a.K;
-  p.act = a.act;
   p.No = a.act >= 0 ? a.N / 2 : a.N;
-  p.beta = a.beta;
-  p.lb = a.linear_beta;
-  p.inv_beta = a.act == MOE_ACT_SITUV2 ? 1.0f / a.beta : 0.0f;
-  p.inv_lb = a.act == MOE_ACT_SITUV2 ? 1.0f / a.linear_beta : 0.0f;
+  p.set(a.act, a.beta, a.linear_beta);
   const int blocks_k = (int)(moe_i8_packed_k(a.K) / 64);
   if (a.act >= 0) run<true>(p, blocks_k, s);
   else run<false>(p, blocks_k, s);

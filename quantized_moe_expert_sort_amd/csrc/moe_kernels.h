@@ -152,6 +152,34 @@ struct NormBackwardArgs {
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
 hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s);
 
+// Layer norm (moe_layer_norm.hip).  Pointers and options as in moe_layer_norm_t; null = not given.
+struct LayerNormArgs {
+  const void* x;           // [T, D] bf16 or fp32
+  const uint16_t* y;       // [T, D] bf16 or null
+  const float* w;          // [D] or null
+  const float* b;          // [D] or null
+  void* h;                 // [T, D] as x, or null
+  uint16_t* n;             // [T, D] bf16 or null
+  void* q;                 // codes or null
+  void* q_scale;
+  float* mean;             // [T], or null
+  float* rstd;             // [T], with mean
+  int T, D, x_dt, q_dt;
+  float eps;
+};
+struct LayerNormBackwardArgs {
+  LayerNormArgs f;         // x, y, w, mean, rstd of the forward call
+  const void* dh;          // [T, D] as x, or null
+  const uint16_t* dn;      // [T, D] bf16
+  void* dx;                // [T, D] as x
+  uint16_t* dy;            // [T, D] bf16 or null
+  float* dw;               // [D] or null
+  float* db;               // [D] or null
+  float* part;             // [MOE_NORM_PARTS, 2, D] partial sums
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t s);
+hipError_t launch_layer_norm_backward(const LayerNormBackwardArgs& a, hipStream_t s);
+
 // Router and balance loss (moe_router.hip), as moe_router_t and moe_balance_t.
 struct RouterArgs {
   const void* logits;      // [T, E] bf16 or fp32
@@ -187,6 +215,30 @@ struct GemmI8Args {
 hipError_t launch_quant_i8(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q, float* scale, hipStream_t s);
 hipError_t launch_pack_i8(const uint8_t* w, int N, int K, uint8_t* out, hipStream_t s);
 hipError_t launch_gemm_i8(const GemmI8Args& a, hipStream_t s);
+
+// Microscaled coding and product (moe_mx.hip, moe_mx_gemm.hip), as moe_quant_mx_t and moe_gemm_mx.
+struct QuantMxArgs {
+  const void* x;           // [rows, cols] bf16 or fp32
+  const uint8_t* noise;    // [rows, cols] or null
+  void* q;                 // codes of the rows, or null
+  uint8_t* q_scale;
+  void* t;                 // codes of the transpose's rows, or null
+  uint8_t* t_scale;
+  int rows, cols, x_dt, q_dt, q_packed, t_dt, t_packed;
+};
+struct GemmMxArgs {
+  const uint8_t* a;        // [T, K] fp8 or [T, K / 2] fp4x2
+  const uint8_t* as;       // [T, K / 32]
+  const uint8_t* w;        // packed
+  const uint8_t* ws;       // packed
+  const void* add;         // [T, No] of the output's type, or null
+  void* out;               // [T, No] bf16 or fp32
+  int T, N, K, a_dt, act, out_dt;   // act < 0: none, No = N; else No = N / 2
+  float beta, linear_beta;
+};
+hipError_t launch_quant_mx(const QuantMxArgs& a, hipStream_t s);
+hipError_t launch_pack_mx(const uint8_t* w, const uint8_t* ws, int N, int K, uint8_t* out, uint8_t* out_scale, hipStream_t s);
+hipError_t launch_gemm_mx(const GemmMxArgs& a, hipStream_t s);
 
 // Word offsets inside the sync array.  Every counter has a 64-byte line of its own: device-scope
 // atomics on one line are serialized (about 11 ns each on gfx950), whatever word they touch.
