@@ -499,6 +499,50 @@ moe_status_t moe_router(const moe_router_t *r, const moe_balance_t *balance, voi
 moe_status_t moe_router_backward(const moe_router_t *r, const moe_balance_t *balance, const float *d_topk_w,
                                  const float *d_loss, void *d_logits, void *stream);
 
+/* Most tokens of moe_routed_few. */
+#define MOE_FEW_MAX_TOKENS 16
+
+/* Tiles of 16 rows: a token has an expert at most once, so each used expert has one. */
+static inline int32_t moe_few_tiles(int32_t tokens, int32_t topk, int32_t num_local_experts) {
+  int64_t n = (int64_t)tokens * topk;
+  return (int32_t)(num_local_experts < n ? num_local_experts : n);
+}
+/* Workspace of moe_routed_few: the layout (as moe_layout_t names it), then that of moe_fused. */
+typedef struct {
+  size_t sorted_ids, expert_ids, row_of, total;
+} moe_few_ws_parts_t;
+static inline moe_few_ws_parts_t moe_few_ws_parts(int32_t tokens, int32_t topk, int32_t num_local_experts) {
+  moe_few_ws_parts_t w;
+  size_t cap = (size_t)moe_few_tiles(tokens, topk, num_local_experts), o = 0;
+  w.sorted_ids = o; o += moe_align256(cap * 16 * 4);
+  w.expert_ids = o; o += moe_align256(cap * 4);
+  w.row_of = o;     o += moe_align256((size_t)tokens * (size_t)topk * 4);
+  w.total = o;
+  return w;
+}
+static inline size_t moe_routed_few_ws_bytes(int32_t tokens, int32_t topk, int32_t num_local_experts, int32_t model_dim,
+                                             int32_t inter_dim, int32_t a_dtype) {
+  return moe_few_ws_parts(tokens, topk, num_local_experts).total +
+         moe_fused_ws_bytes(tokens, model_dim, inter_dim, moe_few_tiles(tokens, topk, num_local_experts), 16, a_dtype, MOE_ACT_SILU);
+}
+
+/* moe_routed_few -- the routed layer of up to MOE_FEW_MAX_TOKENS tokens from their logits: what moe_router,
+ * moe_sort and moe_fused compute, in two launches up to 4 tokens and 32 routed rows (tokens * topk), in three
+ * up to 32 rows and in four beyond, instead of four or five with a layout between them.
+ *   r         as of moe_router; topk_ids and topk_w are written, with the router's choice (the weights may differ
+ *             from its in the last bits).
+ *   x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, act   as of moe_fused (both weights packed) and out_bf16 as
+ *             there: for the ids and weights that are written the same bits.
+ *   expert_begin, num_local_experts   as of moe_sort: chosen experts outside are left out of the sum.
+ *   ws        256-byte aligned scratch of ws_bytes >= moe_routed_few_ws_bytes(...).  Needs no initial value;
+ *             calls that overlap in time need one each.
+ * Shapes and limits as of moe_router and moe_fused; num_local_experts <= num_experts.  x, w1, w2 and out 16-byte,
+ * scales 4-byte aligned (else MOE_ERR_INVALID_ARG).  tokens == 0 returns MOE_OK. */
+moe_status_t moe_routed_few(const moe_router_t *r, const void *x, const uint8_t *x_scale, int32_t a_dtype,
+                            const uint8_t *w1, const uint8_t *w1_scale, const uint8_t *w2, const uint8_t *w2_scale,
+                            int32_t expert_begin, int32_t num_local_experts, int32_t model_dim, int32_t inter_dim,
+                            const moe_act_params_t *act, uint16_t *out_bf16, void *ws, size_t ws_bytes, void *stream);
+
 /* moe_quant_i8 -- symmetric 8-bit coding of bf16 rows, one fp32 scale per row.
  *   x_bf16 [rows, cols], q_out int8 [rows, cols], scale_out [rows]; cols % 16 == 0, pointers to
  *   rows 16-byte aligned (else MOE_ERR_INVALID_ARG).

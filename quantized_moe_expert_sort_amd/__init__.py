@@ -31,7 +31,7 @@ DEBUG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmo
 EXPORTS = ("moe_sort", "moe_quant_act", "moe_pack_w1", "moe_pack_w2", "moe_fused", "moe_fused_noalloc",
            "moe_block_norm", "moe_block_norm_backward", "moe_router", "moe_router_backward", "moe_quant_i8",
            "moe_pack_i8", "moe_gemm_i8", "moe_layer_norm", "moe_layer_norm_backward", "moe_quant_mx", "moe_pack_mx",
-           "moe_gemm_mx", "moe_last_hip_error")
+           "moe_gemm_mx", "moe_routed_few", "moe_last_hip_error")
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 
@@ -130,6 +130,9 @@ def lib():
         L.moe_pack_i8.restype = i32
         L.moe_gemm_i8.argtypes = [vp, vp, vp, vp, i32, i32, i32, ctypes.POINTER(ActParams), vp, vp, vp]
         L.moe_gemm_i8.restype = i32
+        L.moe_routed_few.argtypes = [ctypes.POINTER(RouterParams), vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32,
+                                     ctypes.POINTER(ActParams), vp, vp, sz, vp]
+        L.moe_routed_few.restype = i32
         L.moe_layer_norm.argtypes = [ctypes.POINTER(LayerNormParams), vp]
         L.moe_layer_norm.restype = i32
         L.moe_layer_norm_backward.argtypes = [ctypes.POINTER(LayerNormParams), ctypes.POINTER(LayerNormGradParams), vp, sz, vp]
@@ -670,6 +673,66 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
           _need(w_scale, "w_scale", torch.float32, (N,), index), T, N, K, params,
           _need(add, "add", torch.bfloat16, shape, index), _need(out, "out", torch.bfloat16, shape, index))
     return out
+
+
+# ------------------------------------------------------------------ the routed layer of a few tokens
+
+FEW_MAX_TOKENS = 16
+RoutedFew = collections.namedtuple("RoutedFew", "out ids w")
+
+
+def few_tiles(tokens, topk, num_local_experts):
+    return min(num_local_experts, tokens * topk)
+
+
+def routed_few_ws_bytes(tokens, topk, num_local_experts, model_dim, inter_dim, a_dtype):
+    cap = few_tiles(tokens, topk, num_local_experts)
+    return (_align256(cap * 64) + _align256(cap * 4) + _align256(tokens * topk * 4)
+            + fused_ws_bytes(tokens, model_dim, inter_dim, cap, 16, a_dtype, ACT_SILU))
+
+
+def moe_routed_few(logits, x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, topk, *, expert_begin=0, score="softmax",
+                   renorm=True, scale=1.0, bias=None, valid=None, act="situv2", beta=None, linear_beta=None, out=None, ws=None):
+    """The routed layer of up to FEW_MAX_TOKENS tokens in two to four launches (see moe_routed_few in the
+    header): the choice of moe_router from logits [T, E], then what moe_fused computes of x (bf16 [T, D],
+    or "fp8" / "fp4" codes with x_scale) and the local experts' packed weights (of device_weights).
+
+    Returns RoutedFew(out bf16 [T, D], ids int32 [T, topk], w fp32 [T, topk])."""
+    device, index = _on_gpu(logits, "logits")
+    r, T, _ = _router_params(logits, topk, score, renorm, scale, bias, valid, index)
+    if T > FEW_MAX_TOKENS:
+        raise ValueError(f"logits: at most {FEW_MAX_TOKENS} tokens, got {T} (moe_router, moe_sort and moe_fused take more)")
+    d = _pick(DTYPES, a_dtype, "a_dtype")
+    if w1.dim() != 3 or w2.dim() != 3:
+        raise ValueError(f"w1 and w2: need packed codes [experts, rows, bytes], got {tuple(w1.shape)} and {tuple(w2.shape)}")
+    E, D, I = w2.shape[0], w2.shape[1], 2 * w2.shape[2]
+    _sizes(E, D, I, expert_begin)
+    k = _pick(ACTS, act, "act")
+    if k == ACT_SITUV2 and (beta is None or linear_beta is None):
+        raise ValueError("SiTUv2 needs beta and linear_beta (there are no defaults)")
+    params = ActParams(k, 0.0 if beta is None else beta, 0.0 if linear_beta is None else linear_beta)
+    u8 = torch.uint8
+    if d == DT_BF16:
+        if x_scale is not None:
+            raise ValueError("x_scale: bf16 tokens have none")
+        xp, xsp = _need(x, "x", torch.bfloat16, (T, D), index), None
+    else:
+        xp = _need(x, "x", u8, (T, D if d == DT_FP8 else D // 2), index)
+        xsp = _need(x_scale, "x_scale", u8, (T, D // 32), index)
+        if x_scale is None:
+            raise ValueError(f"x_scale: {a_dtype} tokens need their scales")
+    ids = torch.empty(T, max(topk, 0), dtype=torch.int32, device=device)
+    w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=device)
+    r.topk_ids, r.topk_w = ids.data_ptr(), w.data_ptr()
+    if out is None:
+        out = torch.empty(T, D, dtype=torch.bfloat16, device=device)
+    if ws is None:
+        ws = torch.empty(routed_few_ws_bytes(T, max(topk, 0), E, D, I, d), dtype=u8, device=device)
+    _call("moe_routed_few", index, r, xp, xsp, d, _need(w1, "w1", u8, (E, 2 * I, D // 2), index),
+          _need(w1_scale, "w1_scale", u8, (E, 2 * I, D // 32), index), _need(w2, "w2", u8, (E, D, I // 2), index),
+          _need(w2_scale, "w2_scale", u8, (E, D, I // 32), index), expert_begin, E, D, I, params,
+          _need(out, "out", torch.bfloat16, (T, D), index), _need(ws, "ws", u8, ws.shape, index), ws.numel())
+    return RoutedFew(out, ids, w)
 
 
 # ------------------------------------------------------------------ layer norm

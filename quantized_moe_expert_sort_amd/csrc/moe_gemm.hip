@@ -344,27 +344,6 @@ hipError_t launch_stage2_small(const FusedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Stage tiling per activation dtype and block_m.
-template <int ADT, int BM>
-struct Cfg {
-  // intermediate columns / workgroup: wider at 32-row tiles, where the re-reads of the gathered
-  // activation rows by the workgroups of one tile dominate (fp8/fp4: 64, 3% faster at 1024
-  // tokens; bf16: 32, Stage1 30% faster at 8192 tokens); slower at 16-row tiles
-  static constexpr int NI = BM == 32 ? (ADT == DT_BF16 ? 32 : 64) : (ADT == DT_BF16 ? 16 : 32);
-  static constexpr int KW = 4;                                // waves splitting K in stage1
-  // K steps in flight per wave (the bf16 operands are 4x the fp4 ones in registers; at 64
-  // columns fp8 keeps 2 (3: 272 -> 409 us at 1024 tokens), fp4 takes 3 (468 -> 447 us fused))
-  static constexpr int PF1 = BM == 16 ? 7 : (ADT == DT_FP4 && NI == 64 ? 3 : (ADT == DT_BF16 || NI == 64 ? 2 : 4));
-  static constexpr int MINW1 = 2;                               // waves per SIMD kept
-  // activation rows staged in LDS (fp8 measured faster with its rows in registers)
-  static constexpr bool LDSA = BM == 16 && ADT != DT_FP8;
-  // stage2 16-column fragments / wave (32-row tiles: 4 measured 3% faster than 2 at 1024 tokens
-  // with the packed w2)
-  static constexpr int NF2 = 4;
-  static constexpr int PF2 = 3;                               // K steps in flight (I = 384: all)
-  static constexpr int MINW2 = 2;
-};
-
 template <int ADT, int BM>
 hipError_t run_stages(FusedArgs a, hipStream_t s) {
   using C = Cfg<ADT, BM>;

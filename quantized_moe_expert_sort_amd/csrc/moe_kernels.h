@@ -53,6 +53,7 @@ hipError_t debug_take_sort(uint32_t* v);
 hipError_t debug_take_gemm(uint32_t* v);
 hipError_t debug_take_grouped(uint32_t* v);
 hipError_t debug_take_single(uint32_t* v);
+hipError_t debug_take_few(uint32_t* v);
 #else
 #define MOE_DCHECK(cond, bit) true
 #define MOE_DEBUG_READER(name)
@@ -200,6 +201,11 @@ struct BalanceArgs {
 hipError_t launch_router(const RouterArgs& a, const BalanceArgs* b, void* ws, hipStream_t s);
 hipError_t launch_router_backward(const RouterArgs& a, const BalanceArgs* b, const float* dw, const float* dloss,
                                   void* dlogits, hipStream_t s);
+
+// The routed layer of a few tokens (moe_few.hip): p as for launch_fused with tiles of 16 rows, its layout
+// pointers the ones that are written here, topk_w the router's weights.
+hipError_t launch_routed_few(const FusedArgs& p, const RouterArgs& a, int expert_begin, int32_t* sorted_ids, int32_t* expert_ids,
+                             int32_t* row_of, hipStream_t s);
 
 // Products in 8-bit integers (moe_int8.hip).
 struct GemmI8Args {

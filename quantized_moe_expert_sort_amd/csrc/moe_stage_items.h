@@ -67,14 +67,33 @@ __device__ __forceinline__ int k_hi_of(int D, int w, int KW) {
   return min(D / 128, (w + 1) * ((D / 128 + KW - 1) / KW));
 }
 
+// Stage tiling per activation dtype and block_m.
+template <int ADT, int BM>
+struct Cfg {
+  // intermediate columns / workgroup: wider at 32-row tiles, where the re-reads of the gathered
+  // activation rows by the workgroups of one tile dominate (fp8/fp4: 64, 3% faster at 1024
+  // tokens; bf16: 32, Stage1 30% faster at 8192 tokens); slower at 16-row tiles
+  static constexpr int NI = BM == 32 ? (ADT == DT_BF16 ? 32 : 64) : (ADT == DT_BF16 ? 16 : 32);
+  static constexpr int KW = 4;                                // waves splitting K in stage1
+  // K steps in flight per wave (the bf16 operands are 4x the fp4 ones in registers; at 64
+  // columns fp8 keeps 2 (3: 272 -> 409 us at 1024 tokens), fp4 takes 3 (468 -> 447 us fused))
+  static constexpr int PF1 = BM == 16 ? 7 : (ADT == DT_FP4 && NI == 64 ? 3 : (ADT == DT_BF16 || NI == 64 ? 2 : 4));
+  static constexpr int MINW1 = 2;                               // waves per SIMD kept
+  // activation rows staged in LDS (fp8 measured faster with its rows in registers)
+  static constexpr bool LDSA = BM == 16 && ADT != DT_FP8;
+  // stage2 16-column fragments / wave (32-row tiles: 4 measured 3% faster than 2 at 1024 tokens
+  // with the packed w2)
+  static constexpr int NF2 = 4;
+  static constexpr int PF2 = 3;                               // K steps in flight (I = 384: all)
+  static constexpr int MINW2 = 2;
+};
+
 // ---------------------------------------------------------------- Stage1
 
-// Both items return false without doing anything for a tile with no expert (past num_tiles:
-// the sort writes expert id -1 there), so they can be launched over all cap_tiles tiles.  The
-// tile's row ids and its expert id are loaded together: one memory latency before the weight
-// addresses are known, instead of a chain of dependent loads.
+// The item of tile `tile` whose rows and expert are known: vr, the row ids of this lane's rows
+// 16 f + r16 (anything else than [0, T*topk) marks padding), and e < E.
 template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false>
-__device__ __forceinline__ bool stage1_item(const FusedArgs& p, int tile, int nb,
+__device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb, const int (&vr)[BM / 16], int e,
                                             float (*red)[BM][2 * NI + 1], uint8_t* astage = nullptr) {
   static_assert(!LDSA || BM == 16, "LDS staging is for 16-row tiles");
   constexpr int NT = KW * WAVE;
@@ -91,17 +110,6 @@ __device__ __forceinline__ bool stage1_item(const FusedArgs& p, int tile, int nb
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x / WAVE);   // wave-uniform
   const int r16 = lane & 15, g = lane >> 4;
   const int TK = p.T * p.topk, D = p.D, I = p.I;
-
-  int vr[MF];
-#pragma unroll
-  for (int f = 0; f < MF; ++f) vr[f] = p.sorted_ids[tile * BM + 16 * f + r16];
-  const int e = p.expert_ids[tile];
-  if (e < 0 || e >= p.E) {
-    (void)MOE_DCHECK(e < p.E, DBG_EXPERT);   // -1 marks an unused tile
-    return false;
-  }
-#pragma unroll
-  for (int f = 0; f < MF; ++f) dcheck_row_id(vr[f], TK);
 
   const size_t a_row = (size_t)D * row_bytes_num<ADT>() / row_bytes_den<ADT>();
   const uint8_t* arow[MF];
@@ -350,6 +358,28 @@ __device__ __forceinline__ bool stage1_item(const FusedArgs& p, int tile, int nb
         st<COH>(p.inter_s + (size_t)R * (I / 32) + ocol / 32, (uint8_t)(bad ? 255u : (uint32_t)(sexp + 127)));
     }
   }
+}
+
+// Both items return false without doing anything for a tile with no expert (past num_tiles:
+// the sort writes expert id -1 there), so they can be launched over all cap_tiles tiles.  The
+// tile's row ids and its expert id are loaded together: one memory latency before the weight
+// addresses are known, instead of a chain of dependent loads.
+template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false>
+__device__ __forceinline__ bool stage1_item(const FusedArgs& p, int tile, int nb,
+                                            float (*red)[BM][2 * NI + 1], uint8_t* astage = nullptr) {
+  constexpr int MF = BM / 16;
+  const int r16 = threadIdx.x & 15;
+  int vr[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) vr[f] = p.sorted_ids[tile * BM + 16 * f + r16];
+  const int e = p.expert_ids[tile];
+  if (e < 0 || e >= p.E) {
+    (void)MOE_DCHECK(e < p.E, DBG_EXPERT);   // -1 marks an unused tile
+    return false;
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) dcheck_row_id(vr[f], p.T * p.topk);
+  stage1_rows<ADT, BM, NI, KW, PF, ACT, COH, LDSA>(p, tile, nb, vr, e, red, astage);
   return true;
 }
 

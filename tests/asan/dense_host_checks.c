@@ -1,4 +1,4 @@
-/* Host-side argument checks of layer norm and the microscaled matrices, built with AddressSanitizer on
+/* Host-side argument checks of layer norm, the microscaled matrices and the routed layer of a few tokens, built with AddressSanitizer on
  * the host code of the library (as layer_host_checks.c): every call must be rejected, or finish as a
  * no-op, on the host; the parameter structs are heap blocks of exactly their size. */
 #include <math.h>
@@ -61,8 +61,26 @@ static void mx_checks(void) {
   free(a); free(p);
 }
 
+static void few_checks(void) {
+  moe_router_t *r = (moe_router_t *)calloc(1, sizeof(*r));
+  moe_act_params_t *a = (moe_act_params_t *)calloc(1, sizeof(*a));
+  r->logits = P; r->topk_ids = P; r->topk_w = P;
+  r->tokens = 4; r->num_experts = 8; r->topk = 2; r->scale = 1.f;
+  a->act = MOE_ACT_SILU;
+  EXPECT(moe_routed_few(NULL, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 128, 128, a, P, P, 1 << 30, NULL), MOE_ERR_INVALID_ARG);
+  EXPECT(moe_routed_few(r, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 128, 128, NULL, P, P, 1 << 30, NULL), MOE_ERR_INVALID_ARG);
+  EXPECT(moe_routed_few(r, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 128, 128, a, P, P, 64, NULL), MOE_ERR_WORKSPACE);
+  EXPECT(moe_routed_few(r, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 130, 128, a, P, P, 1 << 30, NULL), MOE_ERR_UNSUPPORTED);
+  r->tokens = MOE_FEW_MAX_TOKENS + 1;
+  EXPECT(moe_routed_few(r, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 128, 128, a, P, P, 1 << 30, NULL), MOE_ERR_UNSUPPORTED);
+  r->tokens = 0;
+  EXPECT(moe_routed_few(r, P, NULL, MOE_DT_BF16, P, P, P, P, 0, 8, 128, 128, a, P, P, 1 << 30, NULL), MOE_OK);
+  free(a); free(r);
+}
+
 int main(void) {
   norm_checks();
+  few_checks();
   mx_checks();
   if (failures) return 1;
   printf("all passed\n");

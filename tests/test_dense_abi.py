@@ -160,3 +160,56 @@ def test_binding_refusals(monkeypatch):
     with pytest.raises(ValueError, match="GPU"):
         monkeypatch.undo()
         qm.moe_layer_norm(x)
+
+
+@no_gpu
+def test_routed_few_refusals():
+    silu = qm.ActParams(1, 0.0, 0.0)
+
+    def call(x=P, xs=None, dt=0, w=P, s=P, begin=0, local=8, d=128, i=128, act=silu, out=P, ws=P, ws_bytes=1 << 30, null=False, **kw):
+        f = dict(logits=P, bias=None, valid=None, topk_ids=P, topk_w=P, tokens=4, num_experts=8, topk=2, dt=0, score=0, renorm=1, scale=1.0)
+        f.update(kw)
+        r = None if null else qm.RouterParams(**f)
+        return qm.lib().moe_routed_few(r, x, xs, dt, w, s, w, s, begin, local, d, i, act, out, ws, ws_bytes, None)
+    for bad in (dict(null=True), dict(tokens=-1), dict(topk=0), dict(num_experts=0), dict(score=2), dict(renorm=2), dict(scale=NAN),
+                dict(logits=None), dict(topk_ids=None), dict(topk_w=None), dict(x=None), dict(w=None), dict(s=None), dict(out=None),
+                dict(ws=None), dict(dt=3), dict(dt=1), dict(xs=P), dict(act=None), dict(act=qm.ActParams(0, 4.0, INF)), dict(local=0),
+                dict(d=0), dict(i=-128), dict(x=P + 8), dict(w=P + 4), dict(s=P + 2), dict(out=P + 2), dict(ws=P + 16),
+                dict(dt=2, xs=P + 1)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(tokens=17), dict(topk=9), dict(num_experts=2049), dict(local=9), dict(d=192), dict(i=64), dict(d=1 << 24),
+                dict(i=1 << 20), dict(act=qm.ActParams(2, 4.0, 25.0))):
+        assert call(**bad) == UNSUPPORTED, bad
+    assert call(ws_bytes=qm.routed_few_ws_bytes(4, 2, 8, 128, 128, 0) - 1) == WORKSPACE
+    assert call(tokens=0, x=None) == OK
+
+
+def test_routed_few_workspace_matches_the_header(tmp_path):
+    cases = [(1, 16, 896, 3584, 384, 0), (16, 16, 896, 3584, 384, 1), (3, 6, 4, 896, 256, 2), (16, 32, 2048, 128, 128, 0), (0, 4, 8, 128, 128, 0)]
+    src = tmp_path / "s.c"
+    src.write_text('#include <stdio.h>\n#include "moe_mi355x.h"\nint main(void) {'
+                   + "".join('printf("%%zu\\n", moe_routed_few_ws_bytes(%d, %d, %d, %d, %d, %d));' % c for c in cases)
+                   + 'printf("%d\\n", MOE_FEW_MAX_TOKENS); return 0; }')
+    exe = tmp_path / "s"
+    subprocess.run(["gcc", "-O1", "-I", os.path.dirname(HEADER), str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(v) for v in got] == [qm.routed_few_ws_bytes(*c) for c in cases] + [qm.FEW_MAX_TOKENS]
+
+
+def test_routed_few_binding_refusals(monkeypatch):
+    monkeypatch.setattr(qm, "_on_gpu", lambda t, name: (t.device, t.get_device()))
+    monkeypatch.setattr(qm, "_call", lambda fn, *args: pytest.fail(f"{fn} was called"))
+    u8 = torch.uint8
+    good = dict(logits=torch.zeros(2, 8), x=torch.zeros(2, 128, dtype=torch.bfloat16), x_scale=None, a_dtype="bf16",
+                w1=torch.zeros(8, 256, 64, dtype=u8), w1_scale=torch.zeros(8, 256, 4, dtype=u8),
+                w2=torch.zeros(8, 128, 64, dtype=u8), w2_scale=torch.zeros(8, 128, 4, dtype=u8), topk=2, act="silu")
+    for match, kw in (("logits", dict(logits=torch.zeros(17, 8))), ("logits", dict(logits=torch.zeros(2, 8, dtype=torch.float16))),
+                      ("x:", dict(x=torch.zeros(2, 128))), ("x:", dict(x=torch.zeros(3, 128, dtype=torch.bfloat16))),
+                      ("a_dtype", dict(a_dtype="i8")), ("x_scale", dict(x_scale=torch.zeros(2, 4, dtype=u8))),
+                      ("x_scale", dict(a_dtype="fp8", x=torch.zeros(2, 128, dtype=u8))), ("w1:", dict(w1=torch.zeros(8, 128, 64, dtype=u8))),
+                      ("w1 and w2", dict(w1=torch.zeros(256, 64, dtype=u8))), ("w2_scale", dict(w2_scale=torch.zeros(8, 128, 3, dtype=u8))),
+                      ("act", dict(act="gelu")), ("SiTUv2", dict(act="situv2")), ("score", dict(score="relu")),
+                      ("out", dict(out=torch.zeros(2, 128))), ("bias", dict(bias=torch.zeros(7))), ("32 bits", dict(topk=1 << 33)),
+                      ("32 bits", dict(expert_begin=1 << 31))):
+        with pytest.raises(ValueError, match=match):
+            qm.moe_routed_few(**{**good, **kw})
