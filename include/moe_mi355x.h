@@ -507,37 +507,45 @@ static inline int32_t moe_few_tiles(int32_t tokens, int32_t topk, int32_t num_lo
   int64_t n = (int64_t)tokens * topk;
   return (int32_t)(num_local_experts < n ? num_local_experts : n);
 }
-/* Workspace of moe_routed_few: the layout (as moe_layout_t names it), then that of moe_fused. */
+/* Workspace of moe_routed_few: byte offsets of its parts (each 256-byte aligned) and the total: the layout
+ * as moe_layout_t names it; the intermediate (two bf16 parts per element for bf16 tokens, else codes and
+ * their scales); beyond MOE_FEW_SMALL_ROWS routed rows their fp32 outputs. */
+#define MOE_FEW_SMALL_ROWS 32
 typedef struct {
-  size_t sorted_ids, expert_ids, row_of, total;
+  size_t sorted_ids, expert_ids, row_of, inter, iscale, rowout, total;
 } moe_few_ws_parts_t;
-static inline moe_few_ws_parts_t moe_few_ws_parts(int32_t tokens, int32_t topk, int32_t num_local_experts) {
+static inline moe_few_ws_parts_t moe_few_ws_parts(int32_t tokens, int32_t topk, int32_t num_local_experts, int32_t model_dim,
+                                                  int32_t inter_dim, int32_t a_dtype) {
   moe_few_ws_parts_t w;
-  size_t cap = (size_t)moe_few_tiles(tokens, topk, num_local_experts), o = 0;
-  w.sorted_ids = o; o += moe_align256(cap * 16 * 4);
+  size_t cap = (size_t)moe_few_tiles(tokens, topk, num_local_experts), rows = cap * 16, o = 0;
+  w.sorted_ids = o; o += moe_align256(rows * 4);
   w.expert_ids = o; o += moe_align256(cap * 4);
   w.row_of = o;     o += moe_align256((size_t)tokens * (size_t)topk * 4);
+  w.inter = o;      o += moe_align256(rows * moe_row_bytes(inter_dim, a_dtype) * (a_dtype == MOE_DT_BF16 ? 2 : 1));
+  w.iscale = o;     o += moe_align256(a_dtype == MOE_DT_BF16 ? 0 : rows * (size_t)(inter_dim / 32));
+  w.rowout = o;     o += (int64_t)tokens * topk > MOE_FEW_SMALL_ROWS ? moe_align256(rows * (size_t)model_dim * 4) : 0;
   w.total = o;
   return w;
 }
 static inline size_t moe_routed_few_ws_bytes(int32_t tokens, int32_t topk, int32_t num_local_experts, int32_t model_dim,
                                              int32_t inter_dim, int32_t a_dtype) {
-  return moe_few_ws_parts(tokens, topk, num_local_experts).total +
-         moe_fused_ws_bytes(tokens, model_dim, inter_dim, moe_few_tiles(tokens, topk, num_local_experts), 16, a_dtype, MOE_ACT_SILU);
+  return moe_few_ws_parts(tokens, topk, num_local_experts, model_dim, inter_dim, a_dtype).total;
 }
 
 /* moe_routed_few -- the routed layer of up to MOE_FEW_MAX_TOKENS tokens from their logits: what moe_router,
  * moe_sort and moe_fused compute, in two launches up to 4 tokens and 32 routed rows (tokens * topk), in three
  * up to 32 rows and in four beyond, instead of four or five with a layout between them.
- *   r         as of moe_router; topk_ids and topk_w are written, with the router's choice (the weights may differ
- *             from its in the last bits).
- *   x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, act   as of moe_fused (both weights packed) and out_bf16 as
- *             there: for the ids and weights that are written the same bits.
+ *   r         as of moe_router; topk_ids and topk_w are written: the router's choice, its weights but for the
+ *             last bits.
+ *   x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, act, out_bf16   as of moe_fused (both weights packed).  The
+ *             output is rounded once: with bf16 tokens the intermediate keeps 17 bits, and the weighted rows are
+ *             added in fp32 (moe_fused rounds both to bf16).
  *   expert_begin, num_local_experts   as of moe_sort: chosen experts outside are left out of the sum.
  *   ws        256-byte aligned scratch of ws_bytes >= moe_routed_few_ws_bytes(...).  Needs no initial value;
  *             calls that overlap in time need one each.
- * Shapes and limits as of moe_router and moe_fused; num_local_experts <= num_experts.  x, w1, w2 and out 16-byte,
- * scales 4-byte aligned (else MOE_ERR_INVALID_ARG).  tokens == 0 returns MOE_OK. */
+ * Shapes and limits as of moe_router and moe_fused; num_local_experts <= num_experts, inter_dim < 2^16, model_dim < 2^24
+ * (else MOE_ERR_UNSUPPORTED).  x, w1, w2 and out 16-byte, scales 4-byte aligned (else MOE_ERR_INVALID_ARG).
+ * tokens == 0 returns MOE_OK. */
 moe_status_t moe_routed_few(const moe_router_t *r, const void *x, const uint8_t *x_scale, int32_t a_dtype,
                             const uint8_t *w1, const uint8_t *w1_scale, const uint8_t *w2, const uint8_t *w2_scale,
                             int32_t expert_begin, int32_t num_local_experts, int32_t model_dim, int32_t inter_dim,

@@ -677,7 +677,7 @@ def moe_gemm_i8(a, a_scale, w_packed, w_scale, *, act=None, beta=None, linear_be
 
 # ------------------------------------------------------------------ the routed layer of a few tokens
 
-FEW_MAX_TOKENS = 16
+FEW_MAX_TOKENS, FEW_SMALL_ROWS = 16, 32
 RoutedFew = collections.namedtuple("RoutedFew", "out ids w")
 
 
@@ -687,8 +687,12 @@ def few_tiles(tokens, topk, num_local_experts):
 
 def routed_few_ws_bytes(tokens, topk, num_local_experts, model_dim, inter_dim, a_dtype):
     cap = few_tiles(tokens, topk, num_local_experts)
-    return (_align256(cap * 64) + _align256(cap * 4) + _align256(tokens * topk * 4)
-            + fused_ws_bytes(tokens, model_dim, inter_dim, cap, 16, a_dtype, ACT_SILU))
+    rows = cap * 16
+    two = 2 if a_dtype == DT_BF16 else 1
+    return (_align256(rows * 4) + _align256(cap * 4) + _align256(tokens * topk * 4)
+            + _align256(rows * row_bytes(inter_dim, a_dtype) * two)
+            + _align256(0 if a_dtype == DT_BF16 else rows * (inter_dim // 32))
+            + (_align256(rows * model_dim * 4) if tokens * topk > FEW_SMALL_ROWS else 0))
 
 
 def moe_routed_few(logits, x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, topk, *, expert_begin=0, score="softmax",

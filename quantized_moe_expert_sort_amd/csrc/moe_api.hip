@@ -162,26 +162,6 @@ moe_status_t moe_quant_act(const uint16_t* x_bf16, int64_t rows, int64_t cols, i
 
 namespace {
 
-// The parts of moe_fused's workspace.
-void set_workspace(moe::FusedArgs* a, void* ws, const moe_fused_ws_parts_t& W, int32_t cap_tiles, int32_t a_dtype, int32_t act) {
-  uint8_t* const base = (uint8_t*)ws;
-  const size_t groups_bytes = moe_align256((size_t)cap_tiles * 8);
-  a->rowout = base + W.rowout;
-  a->groups = (int2*)(base + W.groups);
-  a->num_groups = (int32_t*)(base + W.groups + groups_bytes);
-  a->cgroups = (int2*)(base + W.cgroups);
-  a->num_cgroups = (int32_t*)(base + W.cgroups + groups_bytes);
-  a->tile_hot = (int32_t*)(base + W.tile_hot);
-  a->hot_e = (int32_t*)(base + W.hot_e);
-  a->hotpos = (int32_t*)(base + W.hotpos);
-  a->hotw = (float*)(base + W.hotw);
-  a->hotmask = (uint32_t*)(base + W.hotmask);
-  a->hot_out = base + W.hot_out;
-  a->inter = base + W.inter;
-  a->inter_s = a_dtype == MOE_DT_BF16 ? nullptr : base + W.iscale;
-  a->dbg = act == MOE_ACT_NONE_TEST ? (float*)(base + W.dbg) : nullptr;
-}
-
 // moe_fused and moe_fused_noalloc: the same validation and launches; the no-alloc variant takes
 // its workspace from the scratch array (scratch == true; ws and ws_bytes are ignored).
 moe_status_t fused_call(const void* x, const uint8_t* x_scale, int32_t a_dtype, const uint8_t* w1,
@@ -224,8 +204,10 @@ moe_status_t fused_call(const void* x, const uint8_t* x_scale, int32_t a_dtype, 
   }
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
 
+  uint8_t* base = (uint8_t*)ws;
   const moe_fused_ws_parts_t W = moe_fused_ws_parts(tokens, model_dim, inter_dim, layout->cap_tiles,
                                                     layout->block_m, a_dtype, act->act);
+  const size_t groups_bytes = moe_align256((size_t)layout->cap_tiles * 8);
   moe::FusedArgs a;
   a.x = (const uint8_t*)x;
   a.xs = x_scale;
@@ -237,8 +219,21 @@ moe_status_t fused_call(const void* x, const uint8_t* x_scale, int32_t a_dtype, 
   a.sorted_ids = layout->sorted_token_ids;
   a.expert_ids = layout->expert_ids;
   a.num_tiles = layout->num_tiles;
+  a.rowout = base + W.rowout;
+  a.groups = (int2*)(base + W.groups);
+  a.num_groups = (int32_t*)(base + W.groups + groups_bytes);
+  a.cgroups = (int2*)(base + W.cgroups);
+  a.num_cgroups = (int32_t*)(base + W.cgroups + groups_bytes);
+  a.tile_hot = (int32_t*)(base + W.tile_hot);
+  a.hot_e = (int32_t*)(base + W.hot_e);
+  a.hotpos = (int32_t*)(base + W.hotpos);
+  a.hotw = (float*)(base + W.hotw);
+  a.hotmask = (uint32_t*)(base + W.hotmask);
+  a.hot_out = base + W.hot_out;
   a.row_of = layout->row_of;
-  set_workspace(&a, ws, W, layout->cap_tiles, a_dtype, act->act);
+  a.inter = base + W.inter;
+  a.inter_s = a_dtype == MOE_DT_BF16 ? nullptr : base + W.iscale;
+  a.dbg = act->act == MOE_ACT_NONE_TEST ? (float*)(base + W.dbg) : nullptr;
   a.sync = layout->sync;
   a.out = out_bf16;
   a.T = tokens;
@@ -465,7 +460,7 @@ moe_status_t moe_routed_few(const moe_router_t* r, const void* x, const uint8_t*
     return MOE_ERR_INVALID_ARG;
   if (r->tokens > MOE_FEW_MAX_TOKENS || num_local_experts > r->num_experts || model_dim % 128 != 0 || inter_dim % 128 != 0)
     return MOE_ERR_UNSUPPORTED;
-  if (model_dim >= (1 << 24) || inter_dim >= (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (model_dim >= (1 << 24) || inter_dim >= (1 << 16)) return MOE_ERR_UNSUPPORTED;
   if (r->tokens == 0) return MOE_OK;
   if (!r->topk_ids || !r->topk_w || !x || !w1 || !w1_scale || !w2 || !w2_scale || !out_bf16 || !ws) return MOE_ERR_INVALID_ARG;
   if ((a_dtype == MOE_DT_BF16) != (x_scale == nullptr)) return MOE_ERR_INVALID_ARG;
@@ -473,11 +468,9 @@ moe_status_t moe_routed_few(const moe_router_t* r, const void* x, const uint8_t*
       !aligned4(w2_scale) || ((uintptr_t)ws & 255) != 0)
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_routed_few_ws_bytes(r->tokens, r->topk, num_local_experts, model_dim, inter_dim, a_dtype)) return MOE_ERR_WORKSPACE;
-  const int32_t cap = moe_few_tiles(r->tokens, r->topk, num_local_experts);
-  const moe_few_ws_parts_t L = moe_few_ws_parts(r->tokens, r->topk, num_local_experts);
-  const moe_fused_ws_parts_t W = moe_fused_ws_parts(r->tokens, model_dim, inter_dim, cap, 16, a_dtype, act->act);
+  const moe_few_ws_parts_t L = moe_few_ws_parts(r->tokens, r->topk, num_local_experts, model_dim, inter_dim, a_dtype);
   uint8_t* const base = (uint8_t*)ws;
-  moe::FusedArgs a;
+  moe::FusedArgs a = {};
   a.x = (const uint8_t*)x;
   a.xs = x_scale;
   a.w1 = w1;
@@ -487,23 +480,22 @@ moe_status_t moe_routed_few(const moe_router_t* r, const void* x, const uint8_t*
   a.topk_w = r->topk_w;
   a.sorted_ids = (const int32_t*)(base + L.sorted_ids);
   a.expert_ids = (const int32_t*)(base + L.expert_ids);
-  a.num_tiles = nullptr;
   a.row_of = (const int32_t*)(base + L.row_of);
-  set_workspace(&a, base + L.total, W, cap, a_dtype, act->act);
-  a.sync = nullptr;
+  a.rowout = base + L.rowout;
+  a.inter = base + L.inter;
+  a.inter_s = a_dtype == MOE_DT_BF16 ? nullptr : base + L.iscale;
   a.out = out_bf16;
   a.T = r->tokens;
   a.topk = r->topk;
   a.E = num_local_experts;
   a.D = model_dim;
   a.I = inter_dim;
-  a.cap_tiles = cap;
+  a.cap_tiles = moe_few_tiles(r->tokens, r->topk, num_local_experts);
   a.block_m = 16;
   a.a_dtype = a_dtype;
   a.act = act->act;
   a.beta = act->beta;
   a.linear_beta = act->linear_beta;
-  a.stages = MOE_STAGE_ALL;
   return finish(hip_status(moe::launch_routed_few(a, ra, expert_begin, (int32_t*)(base + L.sorted_ids),
                                                   (int32_t*)(base + L.expert_ids), (int32_t*)(base + L.row_of), (hipStream_t)stream)));
 }

@@ -13,7 +13,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
 
-enum : int { DT_BF16 = 0, DT_FP8 = 1, DT_FP4 = 2 };
+// DT_BF16X2: an intermediate in two bf16 parts (moe_operands.h), of the routed layer of a few tokens
+enum : int { DT_BF16 = 0, DT_FP8 = 1, DT_FP4 = 2, DT_BF16X2 = 5 };
 enum : int { ACT_SITUV2 = 0, ACT_SILU = 1, ACT_NONE = 2 };
 
 // Operand format codes of v_mfma_scale_f32_16x16x128_f8f6f4 (cbsz / blgp fields).

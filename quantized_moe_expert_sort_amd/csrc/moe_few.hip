@@ -2,13 +2,18 @@
 // read, and Stage1 -- in one launch where the batch is small enough that every workgroup can make the
 // choice for itself, with a launch of one workgroup before Stage1 else; then Stage2 and the sum.
 //
+// The stages are those of moe_stage_items.h.  They are bound by the bytes of the weights, which leaves room to
+// keep what lies between them more exactly than moe_fused does: with bf16 tokens the intermediate is stored
+// in two bf16 parts and both are multiplied (in one part its rounding alone is as large as the output's), and
+// the weighted rows are added in fp32 without a rounding of their own.
+//
 // The choice is the router's (moe_router_choice.h), a wave per token, from fp32 copies of the logits.  A
 // token has an expert at most once and there are at most 16 tokens, so every expert that is used has one
 // tile of 16 rows: tile i is the i-th used local expert in ascending order, its rows in ascending token.
 #include "moe_router_choice.h"
 
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is written by the load-to-LDS copies
-#include "moe_stage_items.h"
+#include "moe_stage2_small.h"
 
 namespace moe {
 
@@ -120,86 +125,127 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const RouterArgs a, con
   }
 }
 
-// ---------------------------------------------------------------- choice, layout and Stage1
+// ---------------------------------------------------------------- Stage1, with or without the choice
 //
-// At most 4 tokens and 32 routed rows: each workgroup makes the choice for all of them, a wave per token,
-// and works on the tile that it finds for itself; one more workgroup writes the layout that Stage2 reads.
+// NREG > 0: at most 4 tokens and 32 routed rows; each workgroup makes the choice for all of them, a wave per
+// token, and works on the tile that it finds for itself; one more workgroup writes the layout that Stage2
+// reads.  NREG = 0: the layout is there.
 
-constexpr int FUSED_T = ITEM_WAVES, FUSED_ROWS = 32;
+constexpr int FUSED_T = ITEM_WAVES, FUSED_ROWS = SMALL_ROWS;
 
 template <int ADT, int ACT, int NREG, bool BIAS>
 __global__ __launch_bounds__(ITEM_THREADS, 2) void few_stage1_kernel(const FusedArgs p, const RouterArgs a, const FewLayout o, int n_nblk) {
   using C = Cfg<ADT, 16>;
   static_assert(C::KW == ITEM_WAVES, "Stage1's waves");
-  constexpr int RED = C::KW * 16 * (2 * C::NI + 1) * 4, STAGE = C::LDSA ? C::KW * AStage<ADT, C::PF1>::BYTES : 0;
-  constexpr int RED16 = (RED + 15) / 16 * 16;
+  constexpr int RED = (C::KW * 16 * (2 * C::NI + 1) * 4 + 15) / 16 * 16, STAGE = C::LDSA ? C::KW * AStage<ADT, C::PF1>::BYTES : 0;
   constexpr int ROUTE = FUSED_T * (CAND * 8 + NREG * 64 * 4);
   // Stage1's LDS, and before it the choice's
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RED16 + STAGE > ROUTE ? RED16 + STAGE : ROUTE];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED + STAGE > ROUTE ? RED + STAGE : ROUTE];
   __shared__ int ids[FUSED_ROWS];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // as stage1_kernel: the column blocks of a tile on one XCD; the workgroup before them writes the layout
-  const bool writer = blockIdx.x == 0;
-  const int item = max((int)blockIdx.x - 1, 0), xcd = item & 7, q = item >> 3;
+  constexpr bool CHOOSE = NREG > 0;
+  const bool writer = CHOOSE && blockIdx.x == 0;
+  const int item = CHOOSE ? max((int)blockIdx.x - 1, 0) : (int)blockIdx.x, xcd = item & 7, q = item >> 3;
   const int tq = q / n_nblk, tile = tq * 8 + xcd, nb = q - tq * n_nblk;
   if (tile >= o.cap) return;
-  if (wave < a.T) {
-    int id;
-    float w;
-    route_token<NREG, BIAS>(a, wave, reinterpret_cast<float*>(lds + FUSED_T * CAND * 8) + wave * (NREG * 64),
-                            reinterpret_cast<uint2*>(lds) + wave * CAND, lane, id, w);
-    if (lane < a.K) {
-      ids[wave * a.K + lane] = id;
-      if (writer) {
-        a.ids[wave * a.K + lane] = id;
-        a.w[wave * a.K + lane] = w;
-      }
-    }
-  }
-  __syncthreads();
-  // lane v: routed row v.  Its tile is the number of different local experts below its own.
   const int TK = a.T * a.K;
-  const int e = lane < TK ? local_expert(o, ids[lane]) : -1;
-  int below = 0, pos = 0;
-  for (int v = 0; v < TK; ++v) {
-    const int x = __builtin_amdgcn_readlane(e, v);
-    const uint64_t same = __ballot(e == x);
-    if (x < 0) continue;
-    const bool head = (int)__builtin_ctzll(same) == v;        // counted once per expert
-    below += head && x < e;
-    pos += x == e && v < lane;
-  }
-  const bool local = e >= 0;
-  if (writer) {
-    // each entry by the thread that it falls to: no two stores to one address
-    const int at = local ? below * 16 + pos : -1;
-    for (int i = threadIdx.x; i < o.cap * 16; i += ITEM_THREADS) {
-      int v = TK, x = -1;
-      for (int k = 0; k < TK; ++k) {
-        const int there = __builtin_amdgcn_readlane(at, k);
-        v = there == i ? k : v;
-        x = there == i ? __builtin_amdgcn_readlane(e, k) : x;
+  int vr[1], expert;
+  if constexpr (!CHOOSE) {
+    vr[0] = o.sorted_ids[tile * 16 + (lane & 15)];
+    expert = o.expert_ids[tile];
+    if (!MOE_DCHECK(expert < o.E, DBG_EXPERT) || expert < 0) return;   // -1: an unused tile
+    dcheck_row_id(vr[0], TK);
+  } else {
+    if (wave < a.T) {
+      int id;
+      float w;
+      route_token<NREG, BIAS>(a, wave, reinterpret_cast<float*>(lds + FUSED_T * CAND * 8) + wave * (NREG * 64),
+                              reinterpret_cast<uint2*>(lds) + wave * CAND, lane, id, w);
+      if (lane < a.K) {
+        ids[wave * a.K + lane] = id;
+        if (writer) {
+          a.ids[wave * a.K + lane] = id;
+          a.w[wave * a.K + lane] = w;
+        }
       }
-      o.sorted_ids[i] = v;
-      if ((i & 15) == 0) o.expert_ids[i >> 4] = x;            // a tile's first row is never padding
     }
-    if (wave == 0 && lane < TK) o.row_of[lane] = at;
-    return;
-  }
-  uint64_t mine = __ballot(local && below == tile);           // this tile's rows, in ascending order
-  if (mine == 0) return;                                      // an unused tile; the same in every wave
-  const int expert = __builtin_amdgcn_readlane(e, (int)__builtin_ctzll(mine));
-  int vr[1] = {TK};
+    __syncthreads();
+    // lane v: routed row v.  Its tile is the number of different local experts below its own.
+    const int e = lane < TK ? local_expert(o, ids[lane]) : -1;
+    int below = 0, pos = 0;
+    for (int v = 0; v < TK; ++v) {
+      const int x = __builtin_amdgcn_readlane(e, v);
+      const uint64_t same = __ballot(e == x);
+      if (x < 0) continue;
+      below += (int)__builtin_ctzll(same) == v && x < e;      // counted once per expert
+      pos += x == e && v < lane;
+    }
+    const bool local = e >= 0;
+    if (writer) {
+      // each entry by the thread that it falls to: no two stores to one address
+      const int at = local ? below * 16 + pos : -1;
+      for (int i = threadIdx.x; i < o.cap * 16; i += ITEM_THREADS) {
+        int v = TK, x = -1;
+        for (int k = 0; k < TK; ++k) {
+          const int there = __builtin_amdgcn_readlane(at, k);
+          v = there == i ? k : v;
+          x = there == i ? __builtin_amdgcn_readlane(e, k) : x;
+        }
+        o.sorted_ids[i] = v;
+        if ((i & 15) == 0) o.expert_ids[i >> 4] = x;          // a tile's first row is never padding
+      }
+      if (wave == 0 && lane < TK) o.row_of[lane] = at;
+      return;
+    }
+    uint64_t mine = __ballot(local && below == tile);         // this tile's rows, in ascending order
+    if (mine == 0) return;                                    // an unused tile; the same in every wave
+    expert = __builtin_amdgcn_readlane(e, (int)__builtin_ctzll(mine));
+    vr[0] = TK;
 #pragma unroll
-  for (int j = 0; j < FUSED_T; ++j) {                         // a token has an expert at most once
-    if (mine == 0) break;
-    const int v = (int)__builtin_ctzll(mine);
-    mine &= mine - 1;
-    vr[0] = (lane & 15) == j ? v : vr[0];
+    for (int j = 0; j < FUSED_T; ++j) {                       // a token has an expert at most once
+      if (mine == 0) break;
+      const int v = (int)__builtin_ctzll(mine);
+      mine &= mine - 1;
+      vr[0] = (lane & 15) == j ? v : vr[0];
+    }
   }
-  stage1_rows<ADT, 16, C::NI, C::KW, C::PF1, ACT, false, C::LDSA>(
-      p, tile, nb, vr, expert, reinterpret_cast<float (*)[16][2 * C::NI + 1]>(lds), lds + RED16);
+  stage1_rows<ADT, 16, C::NI, C::KW, C::PF1, ACT, false, C::LDSA, ADT == DT_BF16>(
+      p, tile, nb, vr, expert, reinterpret_cast<float (*)[16][2 * C::NI + 1]>(lds), lds + RED);
 }
+
+// ---------------------------------------------------------------- Stage2 and the sum, more than SMALL_ROWS rows
+
+template <int SDT, bool LDSA>
+__global__ __launch_bounds__(ITEM_THREADS, 2) void few_stage2_kernel(const FusedArgs p) {
+  __shared__ __attribute__((aligned(16))) uint8_t astage[LDSA ? S2Stage<SDT, 16>::BYTES : 16];
+  using C = Cfg<SDT, 16>;
+  auto none = [] {};
+  stage2_item<SDT, 16, C::NF2, C::PF2, false, decltype(none)&, LDSA, true>(p, blockIdx.x % p.cap_tiles, blockIdx.x / p.cap_tiles, none,
+                                                                          astage);
+}
+
+// Thread = four consecutive columns of one token: its rows added in ascending k.
+__global__ __launch_bounds__(256) void few_sum_kernel(const FusedArgs p) {
+  const int groups = p.D / 4, idx = blockIdx.x * 256 + threadIdx.x;
+  if (idx >= p.T * groups) return;
+  const int t = idx / groups, c = (idx - t * groups) * 4;
+  const float* const rows = reinterpret_cast<const float*>(p.rowout) + c;
+  v4f_ sum = {0.f, 0.f, 0.f, 0.f};
+  constexpr int KG = 8;
+  for (int k0 = 0; k0 < p.topk; k0 += KG) {
+    int r[KG];
+    token_rows<KG>(p, t, k0, r);
+    v4f_ v[KG];
+#pragma unroll
+    for (int u = 0; u < KG; ++u) v[u] = r[u] >= 0 ? *reinterpret_cast<const v4f_*>(rows + (size_t)r[u] * p.D) : v4f_{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < KG; ++u) sum += v[u];
+  }
+  *reinterpret_cast<uint2*>(p.out + (size_t)t * p.D + c) = uint2{bf16_pair(sum[0], sum[1]), bf16_pair(sum[2], sum[3])};
+}
+
+// ---------------------------------------------------------------- launches
 
 template <int NREG, bool BIAS>
 hipError_t route(const RouterArgs& a, const FewLayout& o, hipStream_t s) {
@@ -208,20 +254,40 @@ hipError_t route(const RouterArgs& a, const FewLayout& o, hipStream_t s) {
 }
 
 template <int ADT, int ACT, int NREG, bool BIAS>
-hipError_t route_and_stage1(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, hipStream_t s) {
+void stage1(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, hipStream_t s) {
   const int n1 = p.I / Cfg<ADT, 16>::NI;
-  const unsigned grid = (unsigned)((int64_t)(o.cap + 7) / 8 * 8 * n1 + 1);
+  const unsigned grid = (unsigned)((int64_t)(o.cap + 7) / 8 * 8 * n1) + (NREG > 0 ? 1 : 0);
   few_stage1_kernel<ADT, ACT, NREG, BIAS><<<grid, ITEM_THREADS, 0, s>>>(p, a, o, n1);
-  return hipGetLastError();
 }
 template <int ADT, int ACT>
-hipError_t route_and_stage1(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, hipStream_t s) {
-  if (a.E <= 1024) return a.bias ? route_and_stage1<ADT, ACT, 16, true>(p, a, o, s) : route_and_stage1<ADT, ACT, 16, false>(p, a, o, s);
-  return a.bias ? route_and_stage1<ADT, ACT, 32, true>(p, a, o, s) : route_and_stage1<ADT, ACT, 32, false>(p, a, o, s);
+void stage1(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, bool fused, hipStream_t s) {
+  if (!fused) stage1<ADT, ACT, 0, false>(p, a, o, s);
+  else if (a.E <= 1024) a.bias ? stage1<ADT, ACT, 16, true>(p, a, o, s) : stage1<ADT, ACT, 16, false>(p, a, o, s);
+  else a.bias ? stage1<ADT, ACT, 32, true>(p, a, o, s) : stage1<ADT, ACT, 32, false>(p, a, o, s);
 }
 template <int ADT>
-hipError_t route_and_stage1(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, hipStream_t s) {
-  return p.act == ACT_SITUV2 ? route_and_stage1<ADT, ACT_SITUV2>(p, a, o, s) : route_and_stage1<ADT, ACT_SILU>(p, a, o, s);
+hipError_t stages(const FusedArgs& p, const RouterArgs& a, const FewLayout& o, bool fused, hipStream_t s) {
+  if (p.act == ACT_SITUV2) stage1<ADT, ACT_SITUV2>(p, a, o, fused, s);
+  else stage1<ADT, ACT_SILU>(p, a, o, fused, s);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  constexpr int SDT = ADT == DT_BF16 ? DT_BF16X2 : ADT;       // what the intermediate is stored as
+  const int rows = a.T * a.K;
+  if (rows <= SMALL_ROWS) {
+    const unsigned grid = (unsigned)(p.D / 16);
+    if (rows <= 16) stage2_small_kernel<SDT, 16, 16, 1, true><<<grid, 16 * WAVE, 0, s>>>(p);
+    else stage2_small_kernel<SDT, 16, 16, 2, true><<<grid, 16 * WAVE, 0, s>>>(p);
+    return hipGetLastError();
+  }
+  using C = Cfg<SDT, 16>;
+  const int n2 = (p.D + ITEM_WAVES * C::NF2 * 16 - 1) / (ITEM_WAVES * C::NF2 * 16);
+  const unsigned grid = (unsigned)(p.cap_tiles * n2);
+  if (p.I <= S2_I_MAX && p.I <= 128 * C::PF2) few_stage2_kernel<SDT, true><<<grid, ITEM_THREADS, 0, s>>>(p);
+  else few_stage2_kernel<SDT, false><<<grid, ITEM_THREADS, 0, s>>>(p);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  few_sum_kernel<<<(unsigned)((p.T * (p.D / 4) + 255) / 256), 256, 0, s>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -229,18 +295,14 @@ hipError_t route_and_stage1(const FusedArgs& p, const RouterArgs& a, const FewLa
 hipError_t launch_routed_few(const FusedArgs& p, const RouterArgs& a, int expert_begin, int32_t* sorted_ids, int32_t* expert_ids,
                              int32_t* row_of, hipStream_t s) {
   const FewLayout o{sorted_ids, expert_ids, row_of, p.cap_tiles, expert_begin, p.E};
-  FusedArgs rest = p;
-  hipError_t e;
-  if (a.T <= FUSED_T && a.T * a.K <= FUSED_ROWS) {
-    e = p.a_dtype == DT_BF16 ? route_and_stage1<DT_BF16>(p, a, o, s)
-        : p.a_dtype == DT_FP8 ? route_and_stage1<DT_FP8>(p, a, o, s)
-                              : route_and_stage1<DT_FP4>(p, a, o, s);
-    rest.stages = MOE_STAGE_2;
-  } else {
+  hipError_t e = hipSuccess;
+  const bool fused = a.T <= FUSED_T && a.T * a.K <= FUSED_ROWS;
+  if (!fused)
     e = a.E <= 1024 ? (a.bias ? route<16, true>(a, o, s) : route<16, false>(a, o, s))
                     : (a.bias ? route<32, true>(a, o, s) : route<32, false>(a, o, s));
-  }
-  return e != hipSuccess ? e : launch_fused(rest, s);
+  if (e != hipSuccess) return e;
+  if (p.a_dtype == DT_BF16) return stages<DT_BF16>(p, a, o, fused, s);
+  return p.a_dtype == DT_FP8 ? stages<DT_FP8>(p, a, o, fused, s) : stages<DT_FP4>(p, a, o, fused, s);
 }
 
 MOE_DEBUG_READER(few)

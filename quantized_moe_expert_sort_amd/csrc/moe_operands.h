@@ -147,6 +147,32 @@ struct AOperand<DT_BF16> {
   }
 };
 
+// bf16 activations in two parts, v = hi + lo (17 bits of v): a step of a row is its 128 high parts, then
+// its 128 low parts; both are multiplied with the same weights.
+template <>
+struct AOperand<DT_BF16X2> {
+  v8bf a[4], b[4];
+  template <bool COH = false>
+  __device__ __forceinline__ void load(const uint8_t* row, int step, int g, bool valid) {
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const uint8_t* const at = row + step * 512 + 64 * g + 16 * jj;
+      const uint4 q = valid ? ld16<COH>(at) : uint4{0, 0, 0, 0}, r = valid ? ld16<COH>(at + 256) : uint4{0, 0, 0, 0};
+      a[jj] = as_bf16x8(q.x, q.y, q.z, q.w);
+      b[jj] = as_bf16x8(r.x, r.y, r.z, r.w);
+    }
+  }
+  __device__ __forceinline__ void load_lds(const uint8_t* base, int g) { load(base, 0, g, true); }
+  __device__ __forceinline__ v4f mma(const uint4& bq, uint32_t bs, uint32_t, const v4f& c) const {
+    const float sc = e8m0_to_float(bs);
+    const v8bf w[4] = {fp4x8_to_bf16(bq.x, sc), fp4x8_to_bf16(bq.y, sc), fp4x8_to_bf16(bq.z, sc), fp4x8_to_bf16(bq.w, sc)};
+    v4f r = c;
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) r = mfma_bf16(b[jj], w[jj], mfma_bf16(a[jj], w[jj], r));
+    return r;
+  }
+};
+
 // e8m0 scale bytes of one matrix row for a batch of up to PF consecutive 128-deep K steps
 // s0 .. s0+PF-1.  Lane (r16, g) consumes byte 4*s + g of its row for step s, so the four lane
 // groups of a row need the four bytes of one dword per step.  Lane group g loads the dword of
@@ -172,7 +198,10 @@ struct ScaleQuads {
 };
 
 template <int ADT>
-__host__ __device__ constexpr int row_bytes_num() { return ADT == DT_BF16 ? 2 : 1; }
+__host__ __device__ constexpr int row_bytes_num() { return ADT == DT_BF16X2 ? 4 : ADT == DT_BF16 ? 2 : 1; }
+// whether the codes of this type have e8m0 scales
+template <int ADT>
+__host__ __device__ constexpr bool scaled() { return ADT == DT_FP8 || ADT == DT_FP4; }
 template <int ADT>
 __host__ __device__ constexpr int row_bytes_den() { return ADT == DT_FP4 ? 2 : 1; }
 

@@ -92,7 +92,8 @@ struct Cfg {
 
 // The item of tile `tile` whose rows and expert are known: vr, the row ids of this lane's rows
 // 16 f + r16 (anything else than [0, T*topk) marks padding), and e < E.
-template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false>
+// PAIR (bf16 only): the intermediate is stored in two parts, as Stage2 reads DT_BF16X2.
+template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false, bool PAIR = false>
 __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb, const int (&vr)[BM / 16], int e,
                                             float (*red)[BM][2 * NI + 1], uint8_t* astage = nullptr) {
   static_assert(!LDSA || BM == 16, "LDS staging is for 16-row tiles");
@@ -332,8 +333,18 @@ __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb
     if (ADT == DT_BF16) {
       const uint32_t h = f32_to_bf16_rne(y);
       const uint32_t h1 = (uint32_t)__shfl_down((int)h, 1, WAVE);
-      if (valid && (col & 1) == 0)
+      if constexpr (PAIR) {
+        // nothing is left of infinities
+        const uint32_t l = (h & 0x7F80u) == 0x7F80u ? 0u : f32_to_bf16_rne(y - __uint_as_float(h << 16));
+        const uint32_t l1 = (uint32_t)__shfl_down((int)l, 1, WAVE);
+        uint8_t* const at = p.inter + (size_t)R * I * 4 + (ocol >> 7) * 512 + (ocol & 127) * 2;
+        if (valid && (col & 1) == 0) {
+          *reinterpret_cast<uint32_t*>(at) = h | (h1 << 16);
+          *reinterpret_cast<uint32_t*>(at + 256) = l | (l1 << 16);
+        }
+      } else if (valid && (col & 1) == 0) {
         st<COH>(reinterpret_cast<uint32_t*>(p.inter + ((size_t)R * I + ocol) * 2), h | (h1 << 16));
+      }
     } else {
       // the 1x32 rule over the 32 lanes of a block with the hardware converts: an even lane
       // encodes its column and the next (the odd lane's value comes over DPP), then the pairs
@@ -402,7 +413,8 @@ struct S2Stage {
   static constexpr int BYTES = COPIES * 1024;
 };
 
-template <int ADT, int BM, int NF, int PF, bool COH, class Wait, bool LDSA = false>
+// WIDE: the weighted rows are stored in fp32 (rowout holds floats).
+template <int ADT, int BM, int NF, int PF, bool COH, class Wait, bool LDSA = false, bool WIDE = false>
 __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb, Wait&& wait,
                                             uint8_t* astage = nullptr) {
   static_assert(!LDSA || !COH, "the staged rows come from a previous launch");
@@ -448,7 +460,7 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
     const int R = tile * BM + 16 * f + r16;
     aval[f] = (unsigned)vr[f] < (unsigned)TK;
     arow[f] = p.inter + (size_t)R * a_row;
-    asrow[f] = ADT == DT_BF16 ? nullptr : p.inter_s + (size_t)R * (I / 32);
+    asrow[f] = !scaled<ADT>() ? nullptr : p.inter_s + (size_t)R * (I / 32);
   }
   const uint8_t* brow[NF];
   const uint8_t* bsrow[NF];
@@ -504,7 +516,7 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
       for (int j = 0; j < NF; ++j) bsq[j].load(bsrow[j], 0, S, g, true);
 #pragma unroll
       for (int f = 0; f < MF; ++f)
-        if (ADT != DT_BF16) asq[f].load(asrow[f], 0, S, g, aval[f]);
+        if (scaled<ADT>()) asq[f].load(asrow[f], 0, S, g, aval[f]);
 #pragma unroll
       for (int u = 0; u < CPW; ++u) {
         const int c = wv + ITEM_WAVES * u;
@@ -530,7 +542,7 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
 #pragma unroll
           for (int j = 0; j < NF; ++j) bs[j] = bsq[j].get(i, r16, g);
 #pragma unroll
-          for (int f = 0; f < MF; ++f) as[f] = ADT == DT_BF16 ? 0u : asq[f].get(i, r16, g);
+          for (int f = 0; f < MF; ++f) as[f] = !scaled<ADT>() ? 0u : asq[f].get(i, r16, g);
 #pragma unroll
           for (int f = 0; f < MF; ++f)
 #pragma unroll
@@ -563,7 +575,7 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
 #pragma unroll
       for (int i = 0; i < PF; ++i)
         if (s0 + i < S) A[i][f].template load<COH>(arow[f], s0 + i, g, aval[f]);
-      if (ADT != DT_BF16) asq[f].load(asrow[f], s0, S, g, aval[f]);
+      if (scaled<ADT>()) asq[f].load(asrow[f], s0, S, g, aval[f]);
     }
 #pragma unroll
     for (int i = 0; i < PF; ++i) {
@@ -572,7 +584,7 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
 #pragma unroll
         for (int j = 0; j < NF; ++j) bs[j] = bsq[j].get(i, r16, g);
 #pragma unroll
-        for (int f = 0; f < MF; ++f) as[f] = ADT == DT_BF16 ? 0u : asq[f].get(i, r16, g);
+        for (int f = 0; f < MF; ++f) as[f] = !scaled<ADT>() ? 0u : asq[f].get(i, r16, g);
 #pragma unroll
         for (int f = 0; f < MF; ++f)
 #pragma unroll
@@ -594,6 +606,10 @@ __device__ __forceinline__ bool stage2_item(const FusedArgs& p, int tile, int nb
 #pragma unroll
       for (int j = 0; j < NF; ++j) {
         const float o = acc[f][j][i] * wrow[f][i];
+        if constexpr (WIDE) {
+          if (valid) reinterpret_cast<float*>(p.rowout)[R * D + c0 + 16 * j] = o;
+          continue;
+        }
         const uint32_t h = f32_to_bf16_rne(o);
         const uint32_t h1 = (uint32_t)__shfl_down((int)h, 1, WAVE);
         if (valid && (r16 & 1) == 0)

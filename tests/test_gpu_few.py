@@ -1,10 +1,11 @@
-"""The routed layer of a few tokens: choice and weights against float64, the output with the bits of
-moe_sort and moe_fused on the same ids and weights (which the oracle tests hold to float64), and once
-against the oracle itself."""
+"""The routed layer of a few tokens: choice and weights against float64; the output of bf16 tokens
+against float64; that of coded tokens against moe_sort and moe_fused on the same ids and weights (which the
+oracle tests hold to float64), up to the roundings that those have besides."""
 import numpy as np
 import pytest
 import torch
 
+import _dense_ref as dref
 import _layer_ref as lref
 import quantized_moe_expert_sort_amd as qm
 from oracle import moe as om
@@ -22,8 +23,41 @@ def weights(E, D, I):
         b = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)   # noqa: E731
         e = lambda lo, *s: torch.randint(lo, lo + 3, s, generator=g, device="cuda", dtype=torch.int32).to(torch.uint8)   # noqa: E731
         w1, w2 = b(E, 2 * I, D // 2), b(E, D, I // 2)
-        _cache[E, D, I] = (qm.moe_pack_w1(w1), e(119, E, 2 * I, D // 32), qm.moe_pack_w2(w2), e(119, E, D, I // 32))
+        s1, s2 = e(119, E, 2 * I, D // 32), e(119, E, D, I // 32)
+        val = lambda w, s: dref.mx_values(dref.unpairs(w.flatten(0, 1)), s.flatten(0, 1), "fp4").view(E, w.shape[1], -1)   # noqa: E731
+        _cache[E, D, I] = (qm.moe_pack_w1(w1), s1, qm.moe_pack_w2(w2), s2), (val(w1, s1), val(w2, s2))
     return _cache[E, D, I]
+
+
+def float64_output(x, ids, w, values, begin, act):
+    """(out [T, D], bound of its error before the last rounding) by the formulas."""
+    w1, w2 = values
+    E, D, I = w2.shape
+    T, K = ids.shape
+    out, err = torch.zeros(T, D, dtype=torch.float64, device="cuda"), torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    u24 = 2.0 ** -24
+    for t in range(T):
+        xt = x[t].double()
+        for k in range(K):
+            e = int(ids[t, k]) - begin if int(ids[t, k]) >= 0 else -1
+            if not 0 <= e < E:
+                continue
+            r, mag = w1[e] @ xt, w1[e].abs() @ xt.abs()
+            g, u, (mg, mu) = r[:I], r[I:], (2 * u24 * (D / 32 + 16) * mag).split(I)   # roundings of the sums
+            s = torch.sigmoid(g)
+            if act == "silu":
+                y = g * s * u
+                dy = 32 * u24 * (1 + g.abs()) * y.abs()
+            else:
+                tg, tu = torch.tanh(g / 4), torch.tanh(u / 25)
+                y = 100 * tg * s * tu
+                dy = 32 * u24 * 100 * s * (tg.abs() + tu.abs() + (1 + g.abs()) * (tg * tu).abs())   # as _layer_ref.gemm_i8
+            # slopes: at most 1.25 |u| for g, |g| for u; two bf16 parts: a half step of a half step
+            dy = dy + 1.25 * u.abs() * mg + g.abs() * mu + 2.0 ** -16 * y.abs()
+            wk = float(w[t, k])
+            out[t] += wk * (w2[e] @ y)
+            err[t] += abs(wk) * (w2[e].abs() @ (dy + 2 * u24 * (I / 32 + 16 + K) * y.abs()))
+    return out, err
 
 
 def tokens(T, D, a, seed=0):
@@ -34,7 +68,7 @@ def tokens(T, D, a, seed=0):
 
 def check(logits, T, D, I, E, K, a, begin=0, local=None, act=SITU, seed=0, **route):
     local = E if local is None else local
-    w = weights(local, D, I)
+    w, values = weights(local, D, I)
     x, xs = tokens(T, D, a, seed)
     r = qm.moe_routed_few(logits, x, xs, a, *w, K, expert_begin=begin, **route, **act)
     bias, valid = route.get("bias"), route.get("valid")
@@ -46,8 +80,18 @@ def check(logits, T, D, I, E, K, a, begin=0, local=None, act=SITU, seed=0, **rou
                                       lref.counted(logits, valid), 0.0, 0.0)
     # the weights' exponentials, sums of at most 2048 of them and quotient, as of moe_router: 1e-5 relative
     assert ((lref.f64(r.w) - ww).abs() <= 1e-5 * ww.abs() + 1e-37).all()
-    lay = qm.moe_sort(r.ids, r.w, begin, local, 16)
-    assert torch.equal(r.out, qm.moe_fused(x, xs, a, *w, r.w, lay, local, act["act"], act.get("beta"), act.get("linear_beta")))
+    if a == "bf16":
+        out, err = float64_output(x, r.ids.cpu(), r.w.cpu(), values, begin, act["act"])
+        assert ((r.out.double() - out).abs() <= lref.HALF_BF16 * out.abs() + 1.01 * err).all()
+    else:
+        lay = qm.moe_sort(r.ids, r.w, begin, local, 16)
+
+        def fused(weight):
+            return qm.moe_fused(x, xs, a, *w, weight, lay, local, act["act"], act.get("beta"), act.get("linear_beta")).double()
+        # the same codes in between; moe_fused rounds each weighted row, and the sum as it is rounded here
+        rows = sum(fused(r.w * (torch.arange(K, device="cuda") == k)).abs() for k in range(K))
+        want = fused(r.w)
+        assert ((r.out.double() - want).abs() <= lref.HALF_BF16 * (r.out.double().abs() + want.abs() + 1.01 * rows)).all()
     assert torch.isfinite(r.out.float()).all()
     return r
 
@@ -125,7 +169,7 @@ def test_against_the_oracle():
 
 
 def test_caller_buffers_and_no_tokens():
-    w = weights(8, 128, 128)
+    w, _ = weights(8, 128, 128)
     x, _ = tokens(2, 128, "bf16")
     out = torch.full((4, 128), 3.0, device="cuda", dtype=torch.bfloat16)
     ws = torch.full((qm.routed_few_ws_bytes(2, 2, 8, 128, 128, 0),), 255, device="cuda", dtype=torch.uint8)
