@@ -7,6 +7,7 @@ calls raise; there is no fallback path.
 """
 import collections
 import ctypes
+import functools
 import os
 
 import torch
@@ -413,6 +414,11 @@ def _need(t, name, dtype, shape, index):
                      f"{'a dense' if t.is_contiguous() else 'a strided'} {t.dtype} of {tuple(t.shape)} on {t.device}")
 
 
+def _address(t):
+    """The address of one of a call's own tensors, or None."""
+    return None if t is None else t.data_ptr()
+
+
 def _sizes(*values):
     """Refuses sizes that the library's 32-bit arguments cannot hold (ctypes would wrap them)."""
     if max(values) > 0x7FFFFFFF or min(values) < -0x80000000:
@@ -685,6 +691,7 @@ def few_tiles(tokens, topk, num_local_experts):
     return min(num_local_experts, tokens * topk)
 
 
+@functools.lru_cache(maxsize=256)
 def routed_few_ws_bytes(tokens, topk, num_local_experts, model_dim, inter_dim, a_dtype):
     cap = few_tiles(tokens, topk, num_local_experts)
     rows = cap * 16
@@ -749,16 +756,13 @@ def layer_norm_backward_ws_bytes(tokens, dim):
     return _align256(min(max(tokens, 0), NORM_PARTS) * 2 * dim * 4)
 
 
-def _layer_norm_params(x, y, w, eps, index):
+def _layer_norm_rows(x):
+    """(tokens, dim, type of the rows) of x, after its checks."""
     if x.dim() != 2 or x.dtype not in _ROW_TYPES:
         raise ValueError(f"x: need a bfloat16 or float32 tensor [tokens, dim], got {x.dtype} of {tuple(x.shape)}")
     T, D = x.shape
     _sizes(T, D)
-    p = LayerNormParams(tokens=T, dim=D, x_dt=_ROW_TYPES[x.dtype], eps=eps)
-    p.x = _need(x, "x", x.dtype, (T, D), index)
-    p.y = _need(y, "y", torch.bfloat16, (T, D), index)
-    p.w = _need(w, "w", torch.float32, (D,), index)
-    return p, T, D
+    return T, D, _ROW_TYPES[x.dtype]
 
 
 def moe_layer_norm(x, y=None, *, w=None, b=None, eps=1e-5, h=None, want_n=True, q_dtype=None, stats=False):
@@ -769,29 +773,28 @@ def moe_layer_norm(x, y=None, *, w=None, b=None, eps=1e-5, h=None, want_n=True, 
     place), n bf16 (None with want_n=False), q and q_scale for q_dtype "fp8", "fp4" or "i8", stats [2, T]
     with stats=True (the backward pass needs them)."""
     device, index = _on_gpu(x, "x")
-    p, T, D = _layer_norm_params(x, y, w, eps, index)
-    p.b = _need(b, "b", torch.float32, (D,), index)
+    T, D, dt = _layer_norm_rows(x)
+    shape = (T, D)
     n = q = q_scale = st = None
-    if h is not None:
-        p.h = _need(h, "h", x.dtype, (T, D), index)
-    elif y is not None:
+    q_dt = 0
+    if h is None and y is not None:
         h = torch.empty_like(x)
-        p.h = h.data_ptr()
     if want_n:
         n = torch.empty(T, D, dtype=torch.bfloat16, device=device)
-        p.n = n.data_ptr()
     if q_dtype is not None:
-        p.q_dt = _pick(Q_DTYPES, q_dtype, "q_dtype")
-        if p.q_dt == DT_I8:
+        q_dt = _pick(Q_DTYPES, q_dtype, "q_dtype")
+        if q_dt == DT_I8:
             q = torch.empty(T, D, dtype=torch.int8, device=device)
             q_scale = torch.empty(T, dtype=torch.float32, device=device)
         else:
-            q = torch.empty(T, D if p.q_dt == DT_FP8 else D // 2, dtype=torch.uint8, device=device)
+            q = torch.empty(T, D if q_dt == DT_FP8 else D // 2, dtype=torch.uint8, device=device)
             q_scale = torch.empty(T, D // 32, dtype=torch.uint8, device=device)
-        p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
     if stats:
         st = torch.empty(2, T, dtype=torch.float32, device=device)
-        p.stats = st.data_ptr()
+    at = _address
+    p = LayerNormParams(_need(x, "x", x.dtype, shape, index), _need(y, "y", torch.bfloat16, shape, index),
+                        _need(w, "w", torch.float32, (D,), index), _need(b, "b", torch.float32, (D,), index),
+                        _need(h, "h", x.dtype, shape, index), at(n), at(q), at(q_scale), at(st), T, D, dt, q_dt, eps)
     _call("moe_layer_norm", index, p)
     return LayerNorm(h, n, q, q_scale, st)
 
@@ -802,8 +805,10 @@ def moe_layer_norm_backward(x, y, stats, dh, dn, *, w=None, bias=True, dx=None, 
     wanted.  dx: where its gradient goes (as x), which may be dh, or None for a new tensor.
     Returns LayerNormGrads(dx, dy, dw, db), None for what was not given or wanted."""
     device, index = _on_gpu(x, "x")
-    p, T, D = _layer_norm_params(x, y, w, 1.0, index)
-    p.stats = _need(stats, "stats", torch.float32, (2, T), index)
+    T, D, dt = _layer_norm_rows(x)
+    p = LayerNormParams(_need(x, "x", x.dtype, (T, D), index), _need(y, "y", torch.bfloat16, (T, D), index),
+                        _need(w, "w", torch.float32, (D,), index), None, None, None, None, None,
+                        _need(stats, "stats", torch.float32, (2, T), index), T, D, dt, 0, 1.0)
     if dn is None:
         raise ValueError("dn: the gradient of n is needed")
     g = LayerNormGradParams()
@@ -860,22 +865,22 @@ def moe_quant_mx(x, q_dtype=None, *, packed=False, t_dtype=None, t_packed=False,
         raise ValueError(f"x: need a bfloat16 or float32 tensor [rows, cols], got {x.dtype} of {tuple(x.shape)}")
     R, C = x.shape
     _sizes(R, C)
-    p = QuantMxParams(rows=R, cols=C, x_dt=_ROW_TYPES[x.dtype])
-    p.x = _need(x, "x", x.dtype, (R, C), index)
-    p.noise = _need(noise, "noise", torch.uint8, (R, C), index)
     q = q_scale = t = t_scale = None
+    q_dt = t_dt = 0
+    u8 = torch.uint8
     if q_dtype is not None:
-        p.q_dt, p.q_layout = _pick(MX_DTYPES, q_dtype, "q_dtype"), int(bool(packed))
-        shape, s_shape = mx_shapes(R, C, p.q_dt, packed)
-        q, q_scale = (torch.empty(s, dtype=torch.uint8, device=device) for s in (shape, s_shape))
-        p.q, p.q_scale = q.data_ptr(), q_scale.data_ptr()
+        q_dt = _pick(MX_DTYPES, q_dtype, "q_dtype")
+        shape, s_shape = mx_shapes(R, C, q_dt, packed)
+        q, q_scale = torch.empty(shape, dtype=u8, device=device), torch.empty(s_shape, dtype=u8, device=device)
     if t_dtype is not None:
-        p.t_dt, p.t_layout = _pick(MX_DTYPES, t_dtype, "t_dtype"), int(bool(t_packed))
-        shape, s_shape = mx_shapes(C, R, p.t_dt, t_packed)
-        t, t_scale = (torch.empty(s, dtype=torch.uint8, device=device) for s in (shape, s_shape))
-        p.t, p.t_scale = t.data_ptr(), t_scale.data_ptr()
-    if q_dtype is None and t_dtype is None:
+        t_dt = _pick(MX_DTYPES, t_dtype, "t_dtype")
+        shape, s_shape = mx_shapes(C, R, t_dt, t_packed)
+        t, t_scale = torch.empty(shape, dtype=u8, device=device), torch.empty(s_shape, dtype=u8, device=device)
+    elif q_dtype is None:
         raise ValueError("one of q_dtype and t_dtype is needed")
+    at = _address
+    p = QuantMxParams(_need(x, "x", x.dtype, (R, C), index), _need(noise, "noise", u8, (R, C), index), at(q), at(q_scale), at(t),
+                      at(t_scale), R, C, _ROW_TYPES[x.dtype], q_dt, bool(packed), t_dt, bool(t_packed))
     _call("moe_quant_mx", index, p)
     return MxCodes(q, q_scale, t, t_scale)
 

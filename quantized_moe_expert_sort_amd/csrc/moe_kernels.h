@@ -245,6 +245,8 @@ struct GemmMxArgs {
 hipError_t launch_quant_mx(const QuantMxArgs& a, hipStream_t s);
 hipError_t launch_pack_mx(const uint8_t* w, const uint8_t* ws, int N, int K, uint8_t* out, uint8_t* out_scale, hipStream_t s);
 hipError_t launch_gemm_mx(const GemmMxArgs& a, hipStream_t s);
+hipError_t launch_gemm_mx_fp8(const GemmMxArgs& a, hipStream_t s);    // of fp8 tokens, bf16 results
+hipError_t launch_gemm_mx_wide(const GemmMxArgs& a, hipStream_t s);   // of fp8 tokens, fp32 results
 
 // Word offsets inside the sync array.  Every counter has a 64-byte line of its own: device-scope
 // atomics on one line are serialized (about 11 ns each on gfx950), whatever word they touch.

@@ -12,6 +12,7 @@
 // 1 KB of codes, byte 16 (16 g + r) + b = row 16 f + r, columns 128 s + 32 g + 2 b and + 1; and 64 bytes of
 // scales, byte 4 r + g; s fastest; rows past the matrix are zero.
 #include "moe_kernels.h"
+#include "moe_products.h"
 #include "moe_rows.h"
 
 #include <type_traits>
@@ -41,36 +42,40 @@ __device__ __forceinline__ uint8_t* scale_at(const Codes& o, int row, int col) {
 struct Block {             // what the elements of a block share
   int sexp;
   bool bad;                // Inf or NaN: scale 255, codes 0
-  float unit, inv;         // 2^sexp and its reciprocal
+  float inv;               // 2^-sexp
   __device__ __forceinline__ Block(uint32_t amax, int dt) {
     bad = amax >= 0x7F800000u;
     sexp = block_sexp_any(bad ? 0u : amax, dt == MOE_DT_FP8_E4M3 ? Fp8Fmt::EMAX : Fp4Fmt::EMAX);
-    unit = e8m0_scale_float(sexp);
     inv = e8m0_scale_float(-sexp);
   }
   __device__ __forceinline__ uint8_t byte() const { return (uint8_t)(bad ? 255 : sexp + 127); }
 };
 
-// v moved to the neighbour on the element grid that the noise chooses.  Exact but for the sum with the
-// noise, whose 2^-9 steps fp32 holds beside numbers up to 16.
-__device__ __forceinline__ float stochastic(float v, uint32_t noise, const Block& b, int dt) {
+// v / 2^sexp moved to the neighbour on the element grid that byte `k` of `noise` chooses.  Exact but for the sum
+// with the noise, whose 2^-9 steps fp32 holds beside numbers up to 16.
+__device__ __forceinline__ float stochastic(float v, uint32_t noise, int k, const Block& b, int dt) {
   const bool f8 = dt == MOE_DT_FP8_E4M3;
+  const uint32_t mant = f8 ? 3u << 23 : 1u << 23;
   const float a = __builtin_fminf(__builtin_fabsf(v) * b.inv, f8 ? 448.0f : 6.0f);
-  const int e = max((int)(__float_as_uint(a) >> 23) - 127, f8 ? -6 : 0) - (f8 ? 3 : 1);   // exponent of a last place
-  const float t = __builtin_floorf(a * __uint_as_float((uint32_t)(127 - e) << 23) + (float)(2 * noise + 1) * (1.0f / 512.0f));
-  return __builtin_copysignf(t * __uint_as_float((uint32_t)(127 + e) << 23) * b.unit, v);
+  const uint32_t e = max(__float_as_uint(a) & 0x7F800000u, f8 ? 121u << 23 : 127u << 23);   // a's binade, at least the lowest
+  const float up = __builtin_fmaf((float)((noise >> (8 * k)) & 255u), 1.0f / 256.0f, 1.0f / 512.0f);
+  const float t = __builtin_floorf(__builtin_fmaf(a, __uint_as_float((254u << 23) + mant - e), up));
+  return __builtin_copysignf(t * __uint_as_float(e - mant), v);
 }
 
-// Codes of eight values: four bytes (fp4) or eight.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], const Block& b, int dt) {
+// Codes of eight values in units of 2^sexp: four bytes (fp4) or eight.
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], const Block& b, int sexp, int dt) {
   uint2 w = {0, 0};
   if (b.bad) return w;
+  const float unit = e8m0_scale_float(sexp);
   if (dt == MOE_DT_FP8_E4M3) {
-    w.x = encode_pair_fp8_hw(v[0], v[1], b.sexp) | (encode_pair_fp8_hw(v[2], v[3], b.sexp) << 16);
-    w.y = encode_pair_fp8_hw(v[4], v[5], b.sexp) | (encode_pair_fp8_hw(v[6], v[7], b.sexp) << 16);
+    w.x = encode_pair_fp8_hw(v[0], v[1], sexp) | (encode_pair_fp8_hw(v[2], v[3], sexp) << 16);
+    w.y = encode_pair_fp8_hw(v[4], v[5], sexp) | (encode_pair_fp8_hw(v[6], v[7], sexp) << 16);
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) w.x |= encode_pair_fp4_hw(v[2 * j], v[2 * j + 1], b.unit) << (8 * j);
+    w.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w.x, v[0], v[1], unit, 0);   // into one byte each
+    w.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w.x, v[2], v[3], unit, 1);
+    w.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w.x, v[4], v[5], unit, 2);
+    w.x = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w.x, v[6], v[7], unit, 3);
   }
   return w;
 }
@@ -119,10 +124,10 @@ __device__ __forceinline__ void store8(const Codes& o, int row, int col, const f
   if constexpr (NOISE) {
     float s[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = stochastic(v[j], (nz[j / 4] >> (8 * (j % 4))) & 255u, b, o.dt);
-    w = encode8(s, b, o.dt);
+    for (int j = 0; j < 8; ++j) s[j] = stochastic(v[j], nz[j / 4], j % 4, b, o.dt);
+    w = encode8(s, b, 0, o.dt);
   } else {
-    w = encode8(v, b, o.dt);
+    w = encode8(v, b, b.sexp, o.dt);
   }
   uint8_t* const q = code_at(o, row, col);
   if (o.dt == MOE_DT_FP8_E4M3) *reinterpret_cast<uint2*>(q) = w;
@@ -143,29 +148,50 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const XT* __restrict__ 
 }
 
 // Tiles of 128 rows x 64 columns through LDS: the codes of the rows (where asked for) as they are
-// loaded, those of the columns from LDS, a thread taking the 32 rows of one block of one column.
-constexpr int TR = 128, TC = 64;
+// loaded, those of the columns from LDS, a thread taking the 32 rows of one block of one column.  Column c of
+// row r stands at c ^ (16 (r / 32)), so that the four blocks' lanes read distinct banks.
+constexpr int TR = 128, TC = 64, TILE_P = TC + 4;
 template <bool NOISE, class XT>
 __global__ __launch_bounds__(256) void quant_tiles_kernel(const XT* __restrict__ x, const uint8_t* __restrict__ noise, int rows,
                                                           int cols, int tile0, int tiles_c, const Codes o, const Codes ot) {
-  __shared__ float tile[TR][TC + 1];
-  __shared__ uint8_t ntile[NOISE ? TR : 1][TC + 4];
-  const int id = tile0 + (int)blockIdx.x;
+  __shared__ __attribute__((aligned(16))) float tile[TR * TILE_P];
+  __shared__ uint32_t ntile[NOISE ? TR * (TC / 4 + 1) : 1];
+  // neighbouring tiles of a row on one XCD: they share lines of the codes and scales
+  const int id = tile0 + run_of_xcd(blockIdx.x, gridDim.x);
   const int r0 = id / tiles_c * TR, c0 = id % tiles_c * TC;
+  constexpr int PASS = TR / 32;
+  const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;
+  float in[PASS][8];
+  uint32_t nz[PASS][2];
+  if (r0 + TR <= rows && c0 + TC <= cols) {                   // without tests per lane, all loads are in flight together
 #pragma unroll
-  for (int p = 0; p < TR / 32; ++p) {
-    const int r = p * 32 + (threadIdx.x >> 3), c = (threadIdx.x & 7) * 8;
-    float v[8];
-    uint32_t nz[2];
-    load8<NOISE>(x, noise, rows, cols, r0 + r, c0 + c, v, nz);
-    if (o.q) store8<NOISE>(o, r0 + r, c0 + c, v, nz);
+    for (int p = 0; p < PASS; ++p) {
+      const int64_t at = (int64_t)(r0 + p * 32 + lr) * cols + c0 + lc;
+      load_any<8>(x + at, in[p]);
+      if constexpr (NOISE) {
+        const v2u_any n = *reinterpret_cast<const v2u_any*>(noise + at);
+        nz[p][0] = n[0];
+        nz[p][1] = n[1];
+      }
+    }
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      tile[r][c + j] = v[j];
-      if constexpr (NOISE) ntile[r][c + j] = (uint8_t)(nz[j / 4] >> (8 * (j % 4)));
+    for (int p = 0; p < PASS; ++p) load8<NOISE>(x, noise, rows, cols, r0 + p * 32 + lr, c0 + lc, in[p], nz[p]);
+  }
+#pragma unroll
+  for (int p = 0; p < PASS; ++p) {
+    const int r = p * 32 + lr;
+    store_row<8>(tile + r * TILE_P + (lc ^ (16 * p)), in[p]);
+    if constexpr (NOISE) {
+      ntile[r * (TC / 4 + 1) + lc / 4] = nz[p][0];
+      ntile[r * (TC / 4 + 1) + lc / 4 + 1] = nz[p][1];
     }
   }
   __syncthreads();
+  if (o.q) {
+#pragma unroll
+    for (int p = 0; p < PASS; ++p) store8<NOISE>(o, r0 + p * 32 + lr, c0 + lc, in[p], nz[p]);
+  }
   const int c = threadIdx.x >> 2, g = threadIdx.x & 3;       // a column, 32 of its rows
   const int row = c0 + c, col = r0 + 32 * g;                  // of the transpose
   if (row >= ot.rows || col >= ot.kp) return;
@@ -173,20 +199,20 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const XT* __restrict__
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    v[i] = tile[32 * g + i][c];
+    v[i] = tile[(32 * g + i) * TILE_P + (c ^ (16 * g))];
     amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
   const Block b(amax, ot.dt);
   if constexpr (NOISE) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = stochastic(v[i], ntile[32 * g + i][c], b, ot.dt);
+    for (int i = 0; i < 32; ++i) v[i] = stochastic(v[i], ntile[(32 * g + i) * (TC / 4 + 1) + c / 4] >> (8 * (c & 3)), 0, b, ot.dt);
   }
   uint8_t* const q = code_at(ot, row, col);
   uint2 w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const float e[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3], v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
-    w[k] = encode8(e, b, ot.dt);
+    w[k] = encode8(e, b, NOISE ? 0 : b.sexp, ot.dt);
   }
   if (ot.dt == MOE_DT_FP8_E4M3) {
     reinterpret_cast<uint4*>(q)[0] = uint4{w[0].x, w[0].y, w[1].x, w[1].y};
