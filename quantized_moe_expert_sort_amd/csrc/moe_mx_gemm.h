@@ -165,10 +165,12 @@ __device__ __forceinline__ void tile_out(const Gemm& p, const v4f (&acc)[FN][FM]
 // A workgroup takes one 16-channel block (with an activation the gate block and the up block of
 // the same outputs) and 16 tokens; its waves split K and add their sums through LDS.  The weights
 // are read once, from whole lines, straight into the operand registers, STREAM_U blocks (and as many of
-// the gate) in flight per wave before the first product.
+// the gate) in flight per wave before the first product.  Bound by the latency of these loads and of the
+// launch: as many waves as there are K steps, up to 16 (1 x 7168 with SiLU, fp8, us at K 512, 1536, 3584, 7168:
+// 2.9 4.2 5.8 8.5; up to 8 waves 2.9 4.4 6.7 9.3; waves of four steps, up to 8 of them, 3.0 5.6 6.7 9.2).
 
 constexpr int STREAM_U = 4;                   // K steps a wave loads together
-constexpr int STREAM_WAVES = 8;               // waves of a workgroup, at most
+constexpr int STREAM_WAVES = 16;              // waves of a workgroup, at most
 
 template <int ADT, bool ACT>
 __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_mx_stream_kernel(const Gemm p) {
@@ -490,14 +492,14 @@ void run_tiles(const Gemm& p, hipStream_t s) {
 
 // Streamed weights up to 16 tokens, where there is at most a workgroup of 16 channels per CU or at most two
 // tokens: every workgroup reads all the tokens, which beyond costs more than the tiles.  Measured, us, streamed
-// and 32 x 64 tiles, fp8: 1 x 7168 at K 512, 3584, 7168: 2.5 5.8 8.8 and 3.0 6.0 8.9; 8 x 7168 2.6 6.8 11.0 and 3.1 6.0
-// 8.9; 16 x 7168 2.9 8.3 14.5 and 3.1 6.0 9.0; 1 x 3584 2.3 4.4 6.1 and 3.0 5.7 8.7; 16 x 3584 2.5 5.4 9.0 and 3.0 5.9 9.0;
-// 16 x 1000 2.5 5.1 8.6 and 3.1 5.6 8.8.
+// and 32 x 64 tiles, fp8: 1 x 7168 at K 512, 3584, 7168: 2.5 5.6 8.7 and 3.0 6.0 8.9; 8 x 7168 2.6 6.8 11.0 and 3.1 6.0
+// 8.9; 16 x 7168 2.9 8.3 14.5 and 3.1 6.0 9.0; 1 x 3584 2.3 4.3 6.0 and 3.0 5.7 8.7; 16 x 3584 2.6 5.5 9.0 and 3.0 5.9 9.0;
+// 16 x 1000 2.6 5.2 8.6 and 3.1 5.6 8.8; with SiLU 16 x 7168 3.0 6.6 11.2 and 4.0 8.0 12.3.
 template <int ADT, bool ACT>
 void run(const Gemm& p, hipStream_t s) {
   const int groups = (p.No + 15) / 16;
   if (p.T <= 16 && (p.T <= 2 || groups <= 256)) {
-    const int steps = p.K / 128, waves = (steps + STREAM_U - 1) / STREAM_U;
+    const int waves = p.K / 128;                              // a step each, or an equal share
     gemm_mx_stream_kernel<ADT, ACT><<<(unsigned)groups, (waves < STREAM_WAVES ? waves : STREAM_WAVES) * 64, 0, s>>>(p);
   } else {
     run_tiles<ADT, ACT>(p, s);
