@@ -732,17 +732,24 @@ def moe_routed_few(logits, x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, topk
         xsp = _need(x_scale, "x_scale", u8, (T, D // 32), index)
         if x_scale is None:
             raise ValueError(f"x_scale: {a_dtype} tokens need their scales")
-    ids = torch.empty(T, max(topk, 0), dtype=torch.int32, device=device)
-    w = torch.empty(T, max(topk, 0), dtype=torch.float32, device=device)
+    k = max(topk, 0)
+    ids = torch.empty(T, k, dtype=torch.int32, device=device)
+    w = torch.empty(T, k, dtype=torch.float32, device=device)
     r.topk_ids, r.topk_w = ids.data_ptr(), w.data_ptr()
     if out is None:
         out = torch.empty(T, D, dtype=torch.bfloat16, device=device)
+        at = out.data_ptr()
+    else:
+        at = _need(out, "out", torch.bfloat16, (T, D), index)
     if ws is None:
-        ws = torch.empty(routed_few_ws_bytes(T, max(topk, 0), E, D, I, d), dtype=u8, device=device)
+        ws = torch.empty(routed_few_ws_bytes(T, k, E, D, I, d), dtype=u8, device=device)
+        ws_at = ws.data_ptr()
+    else:
+        ws_at = _need(ws, "ws", u8, ws.shape, index)
     _call("moe_routed_few", index, r, xp, xsp, d, _need(w1, "w1", u8, (E, 2 * I, D // 2), index),
           _need(w1_scale, "w1_scale", u8, (E, 2 * I, D // 32), index), _need(w2, "w2", u8, (E, D, I // 2), index),
           _need(w2_scale, "w2_scale", u8, (E, D, I // 32), index), expert_begin, E, D, I, params,
-          _need(out, "out", torch.bfloat16, (T, D), index), _need(ws, "ws", u8, ws.shape, index), ws.numel())
+          at, ws_at, ws.numel())
     return RoutedFew(out, ids, w)
 
 
@@ -777,8 +784,13 @@ def moe_layer_norm(x, y=None, *, w=None, b=None, eps=1e-5, h=None, want_n=True, 
     shape = (T, D)
     n = q = q_scale = st = None
     q_dt = 0
-    if h is None and y is not None:
+    if h is not None:
+        h_at = _need(h, "h", x.dtype, shape, index)
+    elif y is not None:
         h = torch.empty_like(x)
+        h_at = h.data_ptr()
+    else:
+        h_at = None
     if want_n:
         n = torch.empty(T, D, dtype=torch.bfloat16, device=device)
     if q_dtype is not None:
@@ -794,7 +806,7 @@ def moe_layer_norm(x, y=None, *, w=None, b=None, eps=1e-5, h=None, want_n=True, 
     at = _address
     p = LayerNormParams(_need(x, "x", x.dtype, shape, index), _need(y, "y", torch.bfloat16, shape, index),
                         _need(w, "w", torch.float32, (D,), index), _need(b, "b", torch.float32, (D,), index),
-                        _need(h, "h", x.dtype, shape, index), at(n), at(q), at(q_scale), at(st), T, D, dt, q_dt, eps)
+                        h_at, at(n), at(q), at(q_scale), at(st), T, D, dt, q_dt, eps)
     _call("moe_layer_norm", index, p)
     return LayerNorm(h, n, q, q_scale, st)
 
@@ -845,6 +857,7 @@ def mx_padded_k(cols):
     return (cols + 127) // 128 * 128
 
 
+@functools.lru_cache(maxsize=256)
 def mx_shapes(rows, cols, dt, packed=False):
     """Shapes of the codes (uint8) and scales of a matrix [rows, cols] coded along its rows."""
     k = mx_padded_k(cols)
@@ -925,10 +938,13 @@ def moe_gemm_mx(a, a_scale, a_dtype, w, w_scale, out_features, *, act=None, beta
         raise ValueError(f"out_dtype: need bfloat16 or float32, got {out_dtype}")
     shape = (T, N if act is None else N // 2)
     if out is None:
-        out = torch.empty(*shape, dtype=out_dtype, device=device)
+        out = torch.empty(shape, dtype=out_dtype, device=device)
+        at = out.data_ptr()
+    else:
+        at = _need(out, "out", out_dtype, shape, index)
     ws, wss = mx_shapes(N, K, DT_FP4, True)
     _call("moe_gemm_mx", index, _need(a, "a", torch.uint8, a.shape, index),
           _need(a_scale, "a_scale", torch.uint8, (T, K // 32), index), dt, _need(w, "w", torch.uint8, ws, index),
           _need(w_scale, "w_scale", torch.uint8, wss, index), T, N, K, params,
-          _need(add, "add", out_dtype, shape, index), _need(out, "out", out_dtype, shape, index), _ROW_TYPES[out_dtype])
+          _need(add, "add", out_dtype, shape, index), at, _ROW_TYPES[out_dtype])
     return out

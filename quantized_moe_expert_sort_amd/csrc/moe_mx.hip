@@ -11,6 +11,11 @@
 // matrices of any size can be multiplied.  Packed weights are blocks (f, s) of 16 rows x 128 columns:
 // 1 KB of codes, byte 16 (16 g + r) + b = row 16 f + r, columns 128 s + 32 g + 2 b and + 1; and 64 bytes of
 // scales, byte 4 r + g; s fastest; rows past the matrix are zero.
+//
+// Measured on MI355X (medians of traced launches; a 2 GiB copy runs at 4.9 TB/s): along the rows 8192 x 3584 bf16
+// to fp4 16 us (4.7 TB/s), one row 2.2; both ways 4096 x 3584 bf16 to fp4 15.4 us (45 MB: 2.9 TB/s; the passes of a
+// workgroup, load, barrier, codes, overlap only with other workgroups'), 3584 x 3584 fp32 to fp4 18 us (65 MB,
+// 3.6 TB/s; 144 registers, three workgroups on a CU), 777 x 1790 fp32 8.6 us (one workgroup's latency).
 #include "moe_kernels.h"
 #include "moe_products.h"
 #include "moe_rows.h"
@@ -147,19 +152,47 @@ __global__ __launch_bounds__(256) void quant_rows_kernel(const XT* __restrict__ 
   store8<NOISE>(o, row, col, v, nz);
 }
 
-// Tiles of 128 rows x 64 columns through LDS: the codes of the rows (where asked for) as they are
-// loaded, those of the columns from LDS, a thread taking the 32 rows of one block of one column.  Column c of
-// row r stands at c ^ (16 (r / 32)), so that the four blocks' lanes read distinct banks.
-constexpr int TR = 128, TC = 64, TILE_P = TC + 4;
+// Tiles of 128 rows x 64 columns through LDS: the codes of the rows (where asked for) from the registers they
+// were loaded into, those of the columns from LDS.
+//   fp32: a thread takes the 32 rows of one block of one column; column c of row r stands at c ^ (16 (r / 32)),
+//     so that the four blocks' lanes read distinct banks.
+//   bf16: as it came, two columns to a dword, which leaves room for eight workgroups on a CU (4096 x 3584 to
+//     fp4 both ways 15.4 us, with noise 24.5; with fp32 copies, four on a CU, 18.9 and 29.4).  A thread takes 16 rows
+//     of two columns and shares their maxima with its neighbour; the dword's place is turned by the 16-row
+//     group, rows from 64 on change places in pairs.
+constexpr int TR = 128, TC = 64, PASS = TR / 32, TILE_P = TC + 4;
+
+// Codes of 8 n consecutive columns of a row of codes that starts at `col`, and with `lead` their block's scale.
+template <int N, bool NOISE>
+__device__ __forceinline__ void store_column(const Codes& o, int row, int col, const float (&v)[8 * N], const Block& b, bool lead) {
+  if (row >= o.rows || col >= o.kp) return;
+  uint2 w[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float e[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3], v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
+    w[k] = encode8(e, b, NOISE ? 0 : b.sexp, o.dt);
+  }
+  uint8_t* const q = code_at(o, row, col);
+  if (o.dt == MOE_DT_FP8_E4M3) {
+#pragma unroll
+    for (int k = 0; k < N; k += 2) reinterpret_cast<uint4*>(q)[k / 2] = uint4{w[k].x, w[k].y, w[k + 1].x, w[k + 1].y};
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<uint4*>(q) = uint4{w[0].x, w[1].x, w[2].x, w[3].x};
+  } else {
+    *reinterpret_cast<uint2*>(q) = uint2{w[0].x, w[1].x};
+  }
+  if (lead) *scale_at(o, row, col) = b.byte();
+}
+
 template <bool NOISE, class XT>
 __global__ __launch_bounds__(256) void quant_tiles_kernel(const XT* __restrict__ x, const uint8_t* __restrict__ noise, int rows,
                                                           int cols, int tile0, int tiles_c, const Codes o, const Codes ot) {
-  __shared__ __attribute__((aligned(16))) float tile[TR * TILE_P];
+  constexpr bool PAIRS = sizeof(XT) == 2;
+  __shared__ __attribute__((aligned(16))) float tile[PAIRS ? TR * TC / 2 : TR * TILE_P];
   __shared__ uint32_t ntile[NOISE ? TR * (TC / 4 + 1) : 1];
   // neighbouring tiles of a row on one XCD: they share lines of the codes and scales
   const int id = tile0 + run_of_xcd(blockIdx.x, gridDim.x);
   const int r0 = id / tiles_c * TR, c0 = id % tiles_c * TC;
-  constexpr int PASS = TR / 32;
   const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;
   float in[PASS][8];
   uint32_t nz[PASS][2];
@@ -181,7 +214,14 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const XT* __restrict__
 #pragma unroll
   for (int p = 0; p < PASS; ++p) {
     const int r = p * 32 + lr;
-    store_row<8>(tile + r * TILE_P + (lc ^ (16 * p)), in[p]);
+    if constexpr (PAIRS) {                                    // the values are bf16: their upper halves
+      v4u_ w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __builtin_amdgcn_perm(__float_as_uint(in[p][2 * j + 1]), __float_as_uint(in[p][2 * j]), 0x07060302u);
+      *reinterpret_cast<v4u_*>(tile + (r ^ (r >> 6)) * (TC / 2) + ((lc / 2) ^ (8 * ((r >> 4) & 3)))) = w;
+    } else {
+      store_row<8>(tile + r * TILE_P + (lc ^ (16 * p)), in[p]);
+    }
     if constexpr (NOISE) {
       ntile[r * (TC / 4 + 1) + lc / 4] = nz[p][0];
       ntile[r * (TC / 4 + 1) + lc / 4 + 1] = nz[p][1];
@@ -192,35 +232,45 @@ __global__ __launch_bounds__(256) void quant_tiles_kernel(const XT* __restrict__
 #pragma unroll
     for (int p = 0; p < PASS; ++p) store8<NOISE>(o, r0 + p * 32 + lr, c0 + lc, in[p], nz[p]);
   }
-  const int c = threadIdx.x >> 2, g = threadIdx.x & 3;       // a column, 32 of its rows
-  const int row = c0 + c, col = r0 + 32 * g;                  // of the transpose
-  if (row >= ot.rows || col >= ot.kp) return;
-  float v[32];
-  uint32_t amax = 0;
+  if constexpr (PAIRS) {
+    const int k = threadIdx.x & 7, c2 = threadIdx.x >> 3;     // 16-row group, pair of columns
+    float v[2][16];
+    uint32_t amax[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = tile[(32 * g + i) * TILE_P + (c ^ (16 * g))];
-    amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  }
-  const Block b(amax, ot.dt);
-  if constexpr (NOISE) {
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = __float_as_uint(tile[((16 * k + i) ^ (k >> 2)) * (TC / 2) + (c2 ^ (8 * (k & 3)))]);
+      v[0][i] = __uint_as_float(w << 16);
+      v[1][i] = __uint_as_float(w & 0xFFFF0000u);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = stochastic(v[i], ntile[(32 * g + i) * (TC / 4 + 1) + c / 4] >> (8 * (c & 3)), 0, b, ot.dt);
-  }
-  uint8_t* const q = code_at(ot, row, col);
-  uint2 w[4];
+      for (int c = 0; c < 2; ++c) amax[c] = max(amax[c], __float_as_uint(v[c][i]) & 0x7FFFFFFFu);
+    }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float e[8] = {v[8 * k], v[8 * k + 1], v[8 * k + 2], v[8 * k + 3], v[8 * k + 4], v[8 * k + 5], v[8 * k + 6], v[8 * k + 7]};
-    w[k] = encode8(e, b, NOISE ? 0 : b.sexp, ot.dt);
-  }
-  if (ot.dt == MOE_DT_FP8_E4M3) {
-    reinterpret_cast<uint4*>(q)[0] = uint4{w[0].x, w[0].y, w[1].x, w[1].y};
-    reinterpret_cast<uint4*>(q)[1] = uint4{w[2].x, w[2].y, w[3].x, w[3].y};
+    for (int c = 0; c < 2; ++c) {
+      const Block b(max(amax[c], (uint32_t)__builtin_amdgcn_mov_dpp((int)amax[c], DPP_XOR1, 0xF, 0xF, false)), ot.dt);
+      if constexpr (NOISE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          v[c][i] = stochastic(v[c][i], ntile[(16 * k + i) * (TC / 4 + 1) + c2 / 2] >> (16 * (c2 & 1)), c, b, ot.dt);
+      }
+      store_column<2, NOISE>(ot, c0 + 2 * c2 + c, r0 + 16 * k, v[c], b, (k & 1) == 0);
+    }
   } else {
-    *reinterpret_cast<uint4*>(q) = uint4{w[0].x, w[1].x, w[2].x, w[3].x};
+    const int c = threadIdx.x >> 2, g = threadIdx.x & 3;     // a column, 32 of its rows
+    float v[32];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = tile[(32 * g + i) * TILE_P + (c ^ (16 * g))];
+      amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    }
+    const Block b(amax, ot.dt);
+    if constexpr (NOISE) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        v[i] = stochastic(v[i], ntile[(32 * g + i) * (TC / 4 + 1) + c / 4] >> (8 * (c & 3)), 0, b, ot.dt);
+    }
+    store_column<4, NOISE>(ot, c0 + c, r0 + 32 * g, v, b, true);
   }
-  *scale_at(ot, row, col) = b.byte();
 }
 
 // Row-major codes [N, K / 2] and scales [N, K / 32], K a multiple of 32, to the packed layout: a thread
