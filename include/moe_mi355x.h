@@ -700,6 +700,9 @@ moe_status_t moe_pack_mx(const uint8_t *w, const uint8_t *w_scale, int32_t out_f
  *   out       [tokens, out_features], or [tokens, out_features / 2] with act, bf16 or fp32 (out_dtype); bf16 is
  *             rounded once from fp32.
  * A scale byte of 255 (a block that held Inf or NaN) makes its row's or its channel's results NaN.
+ * fp4 tokens: every product keeps its bits, the sums are fp32's.  fp8 tokens, bf16 results: the matrix
+ * instruction adds eight products (columns 8 i .. 8 i + 7) in fixed point, down to 2^-13 of the largest's power of
+ * two; fp32 results are computed from the same values in bf16, without that loss and at half the rate.
  * a and w 16-byte, the scales 4-byte aligned (else MOE_ERR_INVALID_ARG).  in_features < 2^24, tokens < 2^24, packed
  * bytes < 2^32, tokens * max(in_features, out_features) < 2^40 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_gemm_mx(const void *a, const uint8_t *a_scale, int32_t a_dtype, const uint8_t *w, const uint8_t *w_scale,

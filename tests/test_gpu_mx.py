@@ -157,7 +157,7 @@ def eights(a, b):
 
 
 # from streamed weights to the largest tiles; odd numbers of K steps, of tokens and of channels
-SHAPES = [(1, 16, 128), (1, 1000, 640), (3, 77, 3584), (16, 300, 1152), (17, 64, 128), (33, 100, 640), (64, 7168, 256),
+SHAPES = [(1, 16, 128), (1, 1000, 640), (2, 5000, 128), (3, 77, 3584), (9, 5000, 640), (16, 300, 1152), (16, 64, 2304), (17, 64, 128), (33, 100, 640), (64, 7168, 256),
           (100, 333, 896), (250, 2600, 640), (256, 3584, 384), (900, 2100, 640), (1000, 2048, 256), (2100, 2130, 384),
           (2049, 4100, 640)]
 
@@ -178,7 +178,7 @@ def test_product_exact(T, N, K, kind):
     assert out.data_ptr() == into.data_ptr() and torch.equal(out, (want + add.double()).bfloat16())
 
 
-@pytest.mark.parametrize("T,N,K", [(1, 32, 128), (5, 416, 640), (16, 7168, 384), (40, 224, 640), (250, 2592, 384),
+@pytest.mark.parametrize("T,N,K", [(1, 32, 128), (5, 416, 640), (16, 7168, 384), (40, 224, 640), (250, 2592, 384), (600, 2080, 640),
                                    (900, 2112, 640), (2100, 2144, 256), (2049, 4128, 384)])
 @pytest.mark.parametrize("kind", ["fp8", "fp4"])
 @pytest.mark.parametrize("act", ["situv2", "silu"])
