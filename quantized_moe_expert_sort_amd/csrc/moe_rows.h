@@ -155,6 +155,33 @@ __device__ __forceinline__ void store_any(float* p, const float (&v)[VEC]) {
   }
 }
 
+// The same elements as they are in memory, to be unpacked later: what is asked for ahead.
+template <int VEC, class T>
+struct RawRow {
+  static constexpr int N = VEC == 8 ? 2 * (int)sizeof(T) : VEC;  // registers
+  uint32_t w[N];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 8) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const v4u_any_ q = reinterpret_cast<const v4u_any_*>(p)[k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * k + j] = q[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) w[j] = sizeof(T) == 4 ? __float_as_uint((float)p[j]) : (uint32_t)p[j] << 16;
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[VEC]) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      if constexpr (VEC == 8 && sizeof(T) == 2) v[j] = __uint_as_float(j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      else v[j] = __uint_as_float(w[j]);
+    }
+  }
+};
+
 // ------------------------------------------------------------------ int8 codes of a row
 //
 // Symmetric, one fp32 scale per row: scale = amax / 127, code = v * (127 / amax) rounded to
