@@ -10,6 +10,13 @@
 // The choice is the router's (moe_router_choice.h), a wave per token, from fp32 copies of the logits.  A
 // token has an expert at most once and there are at most 16 tokens, so every expert that is used has one
 // tile of 16 rows: tile i is the i-th used local expert in ascending order, its rows in ascending token.
+//
+// Measured on MI355X (medians of traced launches): 1 token, 16 of 896 experts, 3584 x 384, bf16: 12.1 us for choice,
+// layout and Stage1 (Stage1 alone 8.2; a router's and a sort's launch before it 4.7 and 3.4), 6.6 for Stage2 and the sum;
+// 16 tokens, fp8, sigmoid scores with a bias: 11.4 us for choice and layout (16 waves of one CU; 8.3 without the bias,
+// whose keys are ranked in 64 bits; the router's kernel alone, over four CUs, 6.6), 46 Stage1 (374 MB of weights, 8.1 TB/s),
+// 24 Stage2 (187 MB, 7.8 TB/s), 4.6 the sum.  The choice in every workgroup of Stage1 beyond 4 tokens would take a wave
+// several tokens one after the other.
 #include "moe_router_choice.h"
 
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is written by the load-to-LDS copies
