@@ -214,6 +214,36 @@ def test_product_past_2_31_outputs():
         assert torch.equal(out[lo:lo + 300], part)              # K of 128: one product, whatever the tile
 
 
+def whole_codes(rows, K, g):
+    """fp4x2 codes (any byte) and scales of 1: sums of at most 36 K quarters, exact in fp32 for K up to 2^16."""
+    return (torch.randint(0, 256, (rows, K // 2), generator=g, device="cuda", dtype=torch.uint8),
+            torch.full((rows, K // 32), 127, device="cuda", dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("T", [3, 20, 300])
+def test_weights_past_2_31_bytes(T):
+    g = torch.Generator(device="cuda").manual_seed(T)
+    N, K_ = 70_000, 65_536
+    w = torch.randint(0, 256, (N // 16, K_ // 128, 1024), generator=g, device="cuda", dtype=torch.uint8)
+    ws = torch.full((N // 16, K_ // 128, 64), 127, device="cuda", dtype=torch.uint8)
+    a, sa = whole_codes(T, K_, g)
+    out = qm.moe_gemm_mx(a, sa, "fp4", w, ws, N, out_dtype=torch.float32)
+    for lo in (0, 2_100, N // 16 - 40):
+        part = qm.moe_gemm_mx(a, sa, "fp4", w[lo:lo + 40].contiguous(), ws[lo:lo + 40].contiguous(), 640, out_dtype=torch.float32)
+        assert torch.equal(out[:, 16 * lo:16 * lo + 640], part)
+
+
+def test_tokens_past_2_32_bytes():
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, K_, N = 132_000, 65_536, 48
+    a, sa = whole_codes(T, K_, g)
+    w, ws = qm.moe_pack_mx(*whole_codes(N, K_, g))
+    out = qm.moe_gemm_mx(a, sa, "fp4", w, ws, N, out_dtype=torch.float32)
+    for lo in (0, 70_001, T - 200):
+        part = qm.moe_gemm_mx(a[lo:lo + 200].contiguous(), sa[lo:lo + 200].contiguous(), "fp4", w, ws, N, out_dtype=torch.float32)
+        assert torch.equal(out[lo:lo + 200], part)
+
+
 def test_strided_or_mistyped_tensors_are_refused():
     x = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(ValueError, match="strided"):

@@ -103,7 +103,8 @@ def normal(T, E, dt=torch.float32, seed=0):
 @pytest.mark.parametrize("a", ["bf16", "fp8", "fp4"])
 @pytest.mark.parametrize("T,E,K,D,I", [(1, 8, 2, 128, 128), (1, 64, 16, 640, 384), (2, 64, 16, 640, 384), (4, 64, 8, 256, 128),
                                        (3, 40, 6, 896, 256), (4, 5, 5, 128, 512), (5, 40, 6, 128, 128), (16, 64, 16, 512, 128),
-                                       (16, 64, 2, 512, 128), (16, 300, 32, 128, 128), (1, 300, 32, 128, 128), (13, 33, 1, 256, 384)])
+                                       (16, 64, 2, 512, 128), (16, 300, 32, 128, 128), (1, 300, 32, 128, 128), (13, 33, 1, 256, 384),
+                                       (4, 64, 16, 128, 256), (2, 300, 32, 384, 128), (16, 20, 4, 256, 640), (9, 12, 12, 640, 1152)])
 def test_shapes_and_types(a, T, E, K, D, I):
     check(normal(T, E), T, D, I, E, K, a)
     check(normal(T, E, torch.bfloat16), T, D, I, E, K, a, act=dict(act="silu"))
@@ -180,3 +181,18 @@ def test_caller_buffers_and_no_tokens():
     assert e.out.shape == (0, 128)
     with pytest.raises(qm.MoeError, match="WORKSPACE"):
         qm.moe_routed_few(normal(2, 8), x, None, "bf16", *w, 2, ws=ws[:-1], **SITU)
+
+
+@pytest.mark.parametrize("T", [3, 12])
+def test_bad_values_stay_in_their_token(T):
+    # every token takes the same experts, so that a bad one shares its tiles with the others
+    l = torch.zeros(T, 16, device="cuda")
+    w, _ = weights(16, 128, 128)
+    x, _ = tokens(T, 128, "bf16")
+    clean = qm.moe_routed_few(l, x, None, "bf16", *w, 8, **SITU).out
+    for value in (float("nan"), float("inf")):
+        bad = x.clone()
+        bad[1, 5] = value
+        out = qm.moe_routed_few(l, bad, None, "bf16", *w, 8, **SITU).out
+        rest = torch.arange(T) != 1
+        assert not torch.isfinite(out[1].float()).all() and torch.equal(out[rest], clean[rest])
