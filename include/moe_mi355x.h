@@ -538,8 +538,9 @@ static inline size_t moe_routed_few_ws_bytes(int32_t tokens, int32_t topk, int32
  *   r         as of moe_router; topk_ids and topk_w are written: the router's choice, its weights but for the
  *             last bits.
  *   x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, act, out_bf16   as of moe_fused (both weights packed).  The
- *             output is rounded once: with bf16 tokens the intermediate keeps 17 bits, and the weighted rows are
- *             added in fp32 (moe_fused rounds both to bf16).
+ *             output is rounded once: with bf16 tokens the intermediate is stored in 17 bits, and the weighted rows
+ *             are added in fp32 (moe_fused rounds both to bf16).  SiTUv2 is evaluated as in moe_gemm_mx, to 2^-15 of
+ *             its value however small gate and up are.
  *   expert_begin, num_local_experts   as of moe_sort: chosen experts outside are left out of the sum.
  *   ws        256-byte aligned scratch of ws_bytes >= moe_routed_few_ws_bytes(...).  Needs no initial value;
  *             calls that overlap in time need one each.

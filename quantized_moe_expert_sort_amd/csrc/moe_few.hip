@@ -4,8 +4,9 @@
 //
 // The stages are those of moe_stage_items.h.  They are bound by the bytes of the weights, which leaves room to
 // keep what lies between them more exactly than moe_fused does: with bf16 tokens the intermediate is stored
-// in two bf16 parts and both are multiplied (in one part its rounding alone is as large as the output's), and
-// the weighted rows are added in fp32 without a rounding of their own.
+// in two bf16 parts and both are multiplied (in one part its rounding alone is as large as the output's), the
+// weighted rows are added in fp32 without a rounding of their own, and SiTUv2 is the dense products', which
+// keeps its digits next to 0.
 //
 // The choice is the router's (moe_router_choice.h), a wave per token, from fp32 copies of the logits.  A
 // token has an expert at most once and there are at most 16 tokens, so every expert that is used has one
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(ITEM_THREADS, 2) void few_stage1_kernel(const Fused
       vr[0] = (lane & 15) == j ? v : vr[0];
     }
   }
-  stage1_rows<ADT, 16, C::NI, C::KW, C::PF1, ACT, false, C::LDSA, ADT == DT_BF16>(
+  stage1_rows<ADT, 16, C::NI, C::KW, C::PF1, ACT, false, C::LDSA, ADT == DT_BF16, true>(
       p, tile, nb, vr, expert, reinterpret_cast<float (*)[16][2 * C::NI + 1]>(lds), lds + RED);
 }
 

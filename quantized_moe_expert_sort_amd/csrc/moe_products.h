@@ -1,5 +1,5 @@
-// What the dense products share (moe_int8.hip, moe_mx_gemm.hip): the activations of their epilogues, the
-// load-to-LDS copies and the order of tiles.
+// What the dense products share (moe_int8.hip, moe_mx_gemm.hip): the activations of their epilogues (the
+// routed layer of a few tokens has the same), the load-to-LDS copies and the order of tiles.
 #pragma once
 
 #include "moe_device.h"

@@ -26,6 +26,7 @@
 
 #include "moe_kernels.h"
 #include "moe_operands.h"
+#include "moe_products.h"
 
 namespace moe {
 
@@ -93,7 +94,10 @@ struct Cfg {
 // The item of tile `tile` whose rows and expert are known: vr, the row ids of this lane's rows
 // 16 f + r16 (anything else than [0, T*topk) marks padding), and e < E.
 // PAIR (bf16 only): the intermediate is stored in two parts, as Stage2 reads DT_BF16X2.
-template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false, bool PAIR = false>
+// FINE: SiTUv2 as the dense products evaluate it, right however small gate and up are.  situv2, whose bits
+// moe_fused keeps, forms 1 - exp by a difference: where g / beta or u / linear_beta is a small x it is off by up to
+// 2^-25 / x of its value (7% at u = 1e-5, linear_beta 25; beyond a bf16 rounding from x = 8e-6 down).
+template <int ADT, int BM, int NI, int KW, int PF, int ACT, bool COH, bool LDSA = false, bool PAIR = false, bool FINE = false>
 __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb, const int (&vr)[BM / 16], int e,
                                             float (*red)[BM][2 * NI + 1], uint8_t* astage = nullptr) {
   static_assert(!LDSA || BM == 16, "LDS staging is for 16-row tiles");
@@ -329,7 +333,10 @@ __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb
       }
       continue;
     }
-    const float y = ACT == ACT_SITUV2 ? situv2(gs, us, p.beta, inv_beta, p.linear_beta, inv_lb) : silu_mul(gs, us);
+    float y;
+    if constexpr (ACT != ACT_SITUV2) y = silu_mul(gs, us);
+    else if constexpr (FINE) y = situv2_small(gs, us, ActArgs{ACT, p.beta, inv_beta, p.linear_beta, inv_lb});
+    else y = situv2(gs, us, p.beta, inv_beta, p.linear_beta, inv_lb);
     if (ADT == DT_BF16) {
       const uint32_t h = f32_to_bf16_rne(y);
       const uint32_t h1 = (uint32_t)__shfl_down((int)h, 1, WAVE);
