@@ -12,12 +12,19 @@ namespace {
 struct ActArgs {
   int act;                 // < 0: none
   float beta, inv_beta, lb, inv_lb;
-  void set(int a, float b, float l) {
+  float bl;                // beta lb
+  bool apart;              // where that is large and tanh(g / beta) tanh(u / lb) may be below 2^-126: bl is 1, and
+                           // beta and lb go to their own factors
+  // beta tanh(g / beta) is g from beta = 2^100 on (|g| < 2^88), and beta with g's sign up to beta = 2^-100
+  // (|g| > 2^-96): there neither beta nor its inverse grows further, so that nothing leaves fp32's range.
+  __host__ __device__ void set(int a, float b, float l) {
     act = a;
-    beta = b;
-    lb = l;
-    inv_beta = a == MOE_ACT_SITUV2 ? 1.0f / b : 0.0f;
-    inv_lb = a == MOE_ACT_SITUV2 ? 1.0f / l : 0.0f;
+    beta = __builtin_fminf(b, 0x1p100f);
+    lb = __builtin_fminf(l, 0x1p100f);
+    inv_beta = a == MOE_ACT_SITUV2 ? __builtin_fminf(1.0f / beta, 0x1p100f) : 0.0f;
+    inv_lb = a == MOE_ACT_SITUV2 ? __builtin_fminf(1.0f / lb, 0x1p100f) : 0.0f;
+    apart = beta * lb >= 0x1p40f;
+    bl = apart ? 1.0f : beta * lb;
   }
 };
 
@@ -36,7 +43,13 @@ __device__ __forceinline__ float situv2_small(float g, float u, const ActArgs& p
   const float b = __builtin_amdgcn_exp2f(ag * -LOG2E);
   const float c = one_minus_exp2(au * (-2.0f * LOG2E * p.inv_lb));
   const float d = 2.0f - a, den = __builtin_fmaf(d, b, d) * (2.0f - c);
-  const float y = (p.beta * p.lb) * (a * c * (g < 0.0f ? b : 1.0f)) * __builtin_amdgcn_rcpf(den);
+  float ba = a, bc = c;
+  if (p.apart) {
+    asm volatile("");                                         // a scalar branch: as selects 2% of a large product
+    ba *= p.beta;
+    bc *= p.lb;
+  }
+  const float y = p.bl * (ba * bc * (g < 0.0f ? b : 1.0f)) * __builtin_amdgcn_rcpf(den);
   return __builtin_copysignf(y, __uint_as_float(__float_as_uint(g) ^ __float_as_uint(u)));
 }
 __device__ __forceinline__ float activate(const ActArgs& p, float g, float u) {

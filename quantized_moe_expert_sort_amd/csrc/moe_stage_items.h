@@ -311,6 +311,8 @@ __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb
   // Epilogue: thread idx owns column idx % NI of row idx / NI, so the columns of one row sit on
   // consecutive lanes and are packed into 4-byte stores with lane shuffles.
   const float inv_beta = 1.0f / p.beta, inv_lb = 1.0f / p.linear_beta;
+  ActArgs fine;
+  fine.set(ACT, p.beta, p.linear_beta);
   for (int idx = threadIdx.x; idx < BM * NI; idx += NT) {
     const int row = idx / NI, col = idx - row * NI;
     float gs = 0.f, us = 0.f;
@@ -335,7 +337,7 @@ __device__ __forceinline__ void stage1_rows(const FusedArgs& p, int tile, int nb
     }
     float y;
     if constexpr (ACT != ACT_SITUV2) y = silu_mul(gs, us);
-    else if constexpr (FINE) y = situv2_small(gs, us, ActArgs{ACT, p.beta, inv_beta, p.linear_beta, inv_lb});
+    else if constexpr (FINE) y = situv2_small(gs, us, fine);
     else y = situv2(gs, us, p.beta, inv_beta, p.linear_beta, inv_lb);
     if (ADT == DT_BF16) {
       const uint32_t h = f32_to_bf16_rne(y);
