@@ -79,7 +79,10 @@ typedef enum { MOE_STAGE_1 = 1, MOE_STAGE_2 = 2, MOE_STAGE_ALL = 3 } moe_stages_
 typedef enum { MOE_W_ROW_MAJOR = 0, MOE_W1_PACKED = 1, MOE_W_PACKED = 2 } moe_w_layout_t;
 
 /* There are no default betas: PR 4463 "Three tuner defects" item 1 shows two sides silently
- * using different defaults.  beta and linear_beta must be finite and > 0 for SITUV2. */
+ * using different defaults.  beta and linear_beta must be finite and > 0 for SITUV2.  moe_fused
+ * evaluates SITUV2 in plain fp32: each tanh to 2^-25 of itself over its argument x (g / beta or u / linear_beta,
+ * so 2^-9 at x = 2^-16), beta * linear_beta within fp32's range.  moe_gemm_i8, moe_gemm_mx and
+ * moe_routed_few have neither limit. */
 typedef struct {
   int32_t act;          /* moe_act_t */
   float beta;           /* SiTUv2 beta (4.0 on the pages) */
@@ -534,13 +537,16 @@ static inline size_t moe_routed_few_ws_bytes(int32_t tokens, int32_t topk, int32
 
 /* moe_routed_few -- the routed layer of up to MOE_FEW_MAX_TOKENS tokens from their logits: what moe_router,
  * moe_sort and moe_fused compute, in two launches up to 4 tokens and 32 routed rows (tokens * topk), in three
- * up to 32 rows and in four beyond, instead of four or five with a layout between them.
+ * up to 32 rows and in four beyond, instead of four or five with a layout between them.  From 64
+ * routed rows on it takes about as long on the GPU as those three calls.
  *   r         as of moe_router; topk_ids and topk_w are written: the router's choice, its weights but for the
  *             last bits.
  *   x, x_scale, a_dtype, w1, w1_scale, w2, w2_scale, act, out_bf16   as of moe_fused (both weights packed).  The
  *             output is rounded once: with bf16 tokens the intermediate is stored in 17 bits, and the weighted rows
  *             are added in fp32 (moe_fused rounds both to bf16).  SiTUv2 is evaluated as in moe_gemm_mx, to 2^-15 of
- *             its value however small gate and up are.
+ *             its value however small gate and up are.  With fp8 tokens the sums of both stages drop what
+ *             moe_gemm_mx names for bf16 results, and the intermediate's codes move where it lies that near a
+ *             border, as moe_fused's do; there is no form of fp8 tokens without that (bf16 tokens have none of it).
  *   expert_begin, num_local_experts   as of moe_sort: chosen experts outside are left out of the sum.
  *   ws        256-byte aligned scratch of ws_bytes >= moe_routed_few_ws_bytes(...).  Needs no initial value;
  *             calls that overlap in time need one each.
@@ -609,7 +615,8 @@ typedef struct {
  * items) and one pass over the rows:
  *     h = x + y  (x without y);   n = (h - mean(h)) / sqrt(var(h) + eps) * w + b
  * computed in fp32, the variance from the deviations; h, n and q are each rounded once, from fp32 (n and q
- * come from h before its rounding).  Codes, shapes, alignment and Inf / NaN as in moe_block_norm. */
+ * come from h before its rounding).  Codes, shapes, alignment and Inf / NaN as in moe_block_norm.  A row whose
+ * squared deviations sum up beyond fp32's range (deviations from about 1e17 on) has 0 for 1 / deviation. */
 moe_status_t moe_layer_norm(const moe_layer_norm_t *p, void *stream);
 
 typedef struct {
@@ -703,7 +710,8 @@ moe_status_t moe_pack_mx(const uint8_t *w, const uint8_t *w_scale, int32_t out_f
  * A scale byte of 255 (a block that held Inf or NaN) makes its row's or its channel's results NaN.
  * fp4 tokens: every product keeps its bits, the sums are fp32's.  fp8 tokens, bf16 results: the matrix
  * instruction adds eight products (columns 8 i .. 8 i + 7) in fixed point, down to 2^-13 of the largest's power of
- * two; fp32 results are computed from the same values in bf16, without that loss and at half the rate.
+ * two; fp32 results are computed from the same values in bf16, without that loss and at half the rate, and there a
+ * token's or a weight's value below 2^-126 (code times scale) counts as 0.
  * a and w 16-byte, the scales 4-byte aligned (else MOE_ERR_INVALID_ARG).  in_features < 2^24, tokens < 2^24, packed
  * bytes < 2^32, tokens * max(in_features, out_features) < 2^40 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_gemm_mx(const void *a, const uint8_t *a_scale, int32_t a_dtype, const uint8_t *w, const uint8_t *w_scale,

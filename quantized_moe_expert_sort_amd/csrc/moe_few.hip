@@ -15,9 +15,19 @@
 // Measured on MI355X (medians of traced launches): 1 token, 16 of 896 experts, 3584 x 384, bf16: 12.1 us for choice,
 // layout and Stage1 (Stage1 alone 8.2; a router's and a sort's launch before it 4.7 and 3.4), 6.6 for Stage2 and the sum;
 // 16 tokens, fp8, sigmoid scores with a bias: 11.4 us for choice and layout (16 waves of one CU; 8.3 without the bias,
-// whose keys are ranked in 64 bits; the router's kernel alone, over four CUs, 6.6), 46 Stage1 (374 MB of weights, 8.1 TB/s),
-// 24 Stage2 (187 MB, 7.8 TB/s), 4.6 the sum.  The choice in every workgroup of Stage1 beyond 4 tokens would take a wave
-// several tokens one after the other.
+// whose keys are ranked in 64 bits; the router's kernel alone, over four CUs, 6.6), 46 Stage1 (178 different experts,
+// 260 MB of weights, 5.6 TB/s), 24 Stage2 (130 MB, 5.4 TB/s), 4.6 the sum; softmax scores, 223 experts: fp8 8.6,
+// 56 (5.9 TB/s), 29 (5.6 TB/s), 4.6, bf16 8.8, 50 (6.5 TB/s), 37 (4.4 TB/s: two products of each weight), 4.8.  Beyond
+// 1024 experts with a bias the choice keeps 11 registers in scratch.  The choice in every workgroup of Stage1 beyond
+// 4 tokens would take a wave several tokens one after the other.
+//
+// Beside moe_router, moe_sort and moe_fused (the second figure), us, 16 of 896 experts, softmax scores:
+//   tokens                  1            2            4            8            16
+//   bf16, in a graph        18.4  21.6   26.8  28.3   43.2  42.6   63.4  65.6   99.1   98.4
+//   fp8, in a graph         18.7  22.0   28.5  29.9   41.9  43.7   62.8  68.5   99.7  102.2
+//   fp8, called in a row    19    41     29    41     41    44     62    69     99    102
+// The gain is the launches'; with many experts' weights to read there is little, or none: 16 tokens with sigmoid scores
+// and a bias 88.7 and 87.0 (bf16), 88.2 and 90.6 (fp8).
 #include "moe_router_choice.h"
 
 #pragma clang diagnostic ignored "-Winline-asm"   // m0 is written by the load-to-LDS copies

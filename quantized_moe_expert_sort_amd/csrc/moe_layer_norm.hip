@@ -14,8 +14,12 @@
 //
 // Measured on MI355X (medians of traced launches; a 2 GiB copy runs at 4.9 TB/s): forward 8192 x 3584 bf16 with y
 // 41 us (235 MB, 48 us at the copy's rate: a part stays in the last-level cache), 4096 x 3584 with an fp32 stream
-// 36 us (176 MB, 4.9 TB/s), one row 2.7 us; backward 4096 x 3584 fp32 46.7 us (176 MB, 3.8 TB/s: a turn's loads,
-// two sums over the row and stores) and 4.9 for the partial sums; 777 x 1790 bf16 5.1, 7.7 and 4.
+// 36 us (176 MB, 4.9 TB/s), one row 2.7 us; with codes instead of n 8192 x 3584 bf16 fp8 43 us (206 MB, 4.8 TB/s),
+// fp4 41, int8 45 (one reduction more, of the row's largest value), 4096 x 3584 fp32 fp8 32 us (162 MB, 5.0 TB/s);
+// backward 4096 x 3584 fp32 46 us (x, y, dn, dh, dx and dy: 264 MB, 5.7 TB/s, above the copy's rate with the
+// last-level cache's part) and 4.7 for the partial sums; 1000 x 12000 bf16 47 to 49 us (144 MB, 3.0 TB/s: one workgroup
+// of 12 waves a CU, whose loads, sums and stores follow one another, in 128 registers with 3 to 14 more in
+// scratch); 777 x 1790 bf16 5.1, 7.7 and 4.
 #include "moe_norm_rows.h"
 
 namespace moe {
@@ -165,7 +169,7 @@ __global__ __launch_bounds__(1024) void layer_norm_backward_kernel(const LayerNo
     }
   }
   // The next row is asked for as soon as this one is unpacked, where the registers hold both (4096 x 3584 fp32
-  // 50.3 -> 46.7 us); not in wide rows, nor in fp32 rows with a short piece: those would spill.
+  // 50.3 -> 46.7 us); not in wide rows, which spill without it, nor in fp32 rows with a short piece, which would.
   constexpr bool AHEAD = CH == 1 && !(SHORT && sizeof(XT) == 4);
   RawRow<VEC, XT> xr[CH], er[CH];
   RawRow<VEC, uint16_t> yr[CH], ur[CH];

@@ -15,7 +15,8 @@
 // Measured on MI355X (medians of traced launches; a 2 GiB copy runs at 4.9 TB/s): along the rows 8192 x 3584 bf16
 // to fp4 16 us (4.7 TB/s), one row 2.2; both ways 4096 x 3584 bf16 to fp4 15.4 us (45 MB: 2.9 TB/s; the passes of a
 // workgroup, load, barrier, codes, overlap only with other workgroups'), 3584 x 3584 fp32 to fp4 18 us (65 MB,
-// 3.6 TB/s; 144 registers, three workgroups on a CU), 777 x 1790 fp32 8.6 us (one workgroup's latency).
+// 3.6 TB/s; 144 registers, three workgroups on a CU), 777 x 1790 fp32 8.6 us (one workgroup's latency); with noise
+// 4096 x 3584 bf16 21 to 24 us (60 MB, 2.5 to 2.8 TB/s), fp32 28 us (89 MB, 3.2 TB/s; 216 registers, two workgroups).
 #include "moe_kernels.h"
 #include "moe_products.h"
 #include "moe_rows.h"

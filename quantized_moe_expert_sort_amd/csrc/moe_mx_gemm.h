@@ -261,7 +261,8 @@ __global__ __launch_bounds__(STREAM_WAVES * 64) void gemm_mx_stream_kernel(const
 // the products 274; without the scales' copies, whose rows are 8 bytes to a line, 298.  No faster: operands read a unit
 // ahead (324 us, 244 registers), four waves of 128 x 128 (324), a higher priority of the products, copies later
 // in the step (320); two fours of waves that take turns at reading and multiplying (fp8 443 us); weights straight
-// from the L2 into registers (553 us: their latency shows).
+// from the L2 into registers (553 us: their latency shows); a third buffer for fp8 (warm operands: 8192^3 405 us where
+// two take 400, 8192 x 7168 x 3584 170 and 167).
 
 template <int BM, int BN, int GM, int GN, int S, int KG, int ADT, bool ACT>
 struct Tile {
@@ -480,6 +481,10 @@ void tile(const Gemm& p, hipStream_t s) {
 //       384 x 7168 42.8 29.9 33.0 [25.7] 38.1   1024 x 7168 98.4 66.1 65.6 51.4 [42.1]
 //   fp8, K 3584:  64 x 7168 [6.5] 8.4 10.1 16.3 24.6   256 x 3584 11.4 [9.0] 10.7 17.5 25.9   256 x 7168 20.9 13.6 [13.6] 17.8 26.3
 //       384 x 7168 30.1 19.5 20.0 [18.1] 26.6   1024 x 7168 68.7 40.2 39.1 35.3 [30.6]
+// The rule counts workgroups only, and small batches of very wide weights lie outside the table: past 16384 rows
+// 3 to 64 tokens go to 128 x 128 tiles and past 32768 to 256 x 256, which they hardly fill.  As chosen, K 3584, 16 tokens, rows
+// 16384, 16400, 28672, 32768, 32784, 65536: fp4 8.0 13.3 14.4 15.1 27.3 41, fp8 7.9 16.9 17.6 18.5 39.3 52.  Against them
+// only calls of 8192 rows each were measured: 32768 rows 23 (fp4) and 24 (fp8), 65536 rows 56 and 59.
 template <int ADT, bool ACT>
 void run_tiles(const Gemm& p, hipStream_t s) {
   constexpr int CUS = 256;
